@@ -399,6 +399,121 @@ kdn_status kdn_backward_kept_events(const kdn_desc *d, const void *q, const void
                                     float *dr, float *dlambda0, float *dS0, void *ws,
                                     size_t ws_bytes, void *stream, void *const *events);
 
+/* ------------------------------------------------- norm and 8-bit operands
+ * What stands around the KDN layer in a model ("Kalman Delta Networks", English
+ * abstract: the layer replaces linear attention inside language models): the
+ * norm before it, and its projections in 8 bits.
+ *
+ * The 8-bit format: e4m3 without infinities (largest value 448), with one
+ * float32 scale per block of 128 columns of one row (activations) or per block
+ * of 128 x 128 (weights); the last block of a row or column may be shorter.
+ * value = element * scale, scale = max(max |value| / 448, 2^-126), and elements
+ * are rounded to nearest even.  A block that holds a NaN has a NaN scale, one
+ * that holds an infinity an infinite scale. */
+
+/* rows x d, dense rows.  dtype: x, y and dy; residual_dtype: residual and s
+ * (KDN_F32 or dtype).  d a multiple of 8 up to 16384, rows up to 2^24 - 1
+ * (KDN_ERR_UNSUPPORTED otherwise); eps >= 0. */
+typedef struct {
+    int64_t rows;
+    int32_t d;
+    int32_t dtype;          /* kdn_dtype */
+    int32_t residual_dtype; /* kdn_dtype */
+    float eps;
+} kdn_norm_desc;
+
+/* RMS norm with the residual's addition:
+ *   s = x + residual, rounded to residual_dtype (residual NULL: s is x)
+ *   rstd = (mean_j s_j^2 + eps)^(-1/2),   y = s rstd weight
+ * of s as stored, in float32, rounded once.  weight [d] float32; y [rows, d];
+ * s [rows, d]: given exactly if residual is, and may be the residual's own
+ * buffer; rstd [rows] float32 or NULL, for the backward.  y must not alias an
+ * input.  x, residual, weight, y and s 16-byte aligned.  The sum of squares of
+ * a row must be a float32. */
+kdn_status kdn_rms_norm(const kdn_norm_desc *n, const void *x, const void *residual,
+                        const float *weight, void *y, void *s, float *rstd, void *stream);
+
+/* The same with y in 8 bits (from float32, not by way of dtype): q [rows, d]
+ * e4m3 and scale [rows, ceil(d / 128)] float32, an operand of kdn_quant_gemm. */
+kdn_status kdn_rms_norm_quant(const kdn_norm_desc *n, const void *x, const void *residual,
+                              const float *weight, void *q, float *scale, void *s, float *rstd,
+                              void *stream);
+
+/* Bytes of workspace kdn_rms_norm_backward needs (0 if the descriptor is
+ * invalid).  Host-only. */
+size_t kdn_rms_norm_backward_workspace_bytes(const kdn_norm_desc *n);
+
+/* Backward of the norm: from dy (dtype), the s and rstd that the forward left
+ * (without a residual: s is x, in residual_dtype = dtype) and ds, the gradient
+ * that reaches the residual stream s from elsewhere (float32; NULL: zero),
+ *   dx [rows, d]   the gradient of s, hence of x and of residual
+ *   dweight [d]
+ * float32 whatever the inputs' types.  The sum over rows is taken in a fixed
+ * order: the same call gives the same bits.  dx may be ds's own buffer; no other
+ * output may alias an input.  Pointers but rstd and dweight 16-byte aligned. */
+kdn_status kdn_rms_norm_backward(const kdn_norm_desc *n, const void *dy, const void *s,
+                                 const float *weight, const float *rstd, const float *ds,
+                                 float *dx, float *dweight, void *ws, size_t ws_bytes,
+                                 void *stream);
+
+/* x [rows, d] (dtype) in 8 bits: q [rows, d] and scale [ceil(rows / block_rows),
+ * ceil(d / 128)], block_rows 1 or 128.  d a multiple of 8; at most 2^24 - 1
+ * blocks of 128 x 128, or of 16 rows' blocks of 128.  x and q 16-byte aligned. */
+typedef struct {
+    int64_t rows;
+    int32_t d;
+    int32_t block_rows;
+    int32_t dtype; /* kdn_dtype */
+} kdn_quant_desc;
+kdn_status kdn_quantize(const kdn_quant_desc *n, const void *x, void *q, float *scale,
+                        void *stream);
+
+/* ------------------------------------------------------- gated recurrence
+ * The linear recurrence without a key space, h_t = a_t h_{t-1} + x_t for each
+ * channel, as it is stacked with KDN layers: the token maps h -> a h + x compose
+ * associatively, as the Moebius maps of the precision recurrence do (same
+ * pages: log-depth associative scans).
+ *   x, a, h [B,H,T,d]; h0, h_T [B,H,d] float32.
+ * dtype: x and h; gate_dtype: a.  d a multiple of 8 up to 2^20, T up to 2^30,
+ * B*H up to 2^24 - 1, and at most 2^24 - 1 workgroups (KDN_ERR_UNSUPPORTED
+ * otherwise).  State and sums are float32.  Every pointer 16-byte aligned.
+ * |a| <= 1 is expected (not checked): products of a over a run of tokens are
+ * formed, and must stay in float32's range.  a_t = 0 starts anew at token t. */
+typedef struct {
+    int32_t B, H, T, d;
+    int32_t dtype;      /* kdn_dtype */
+    int32_t gate_dtype; /* kdn_dtype */
+} kdn_scan_desc;
+
+/* Bytes of workspace kdn_gated_scan / kdn_gated_scan_backward need (0 if the
+ * descriptor is invalid).  Host-only. */
+size_t kdn_gated_scan_workspace_bytes(const kdn_scan_desc *s);
+size_t kdn_gated_scan_backward_workspace_bytes(const kdn_scan_desc *s);
+
+/* The recurrence from h0 (NULL: zeros).  h_T: NULL or the state after the last
+ * token (h0 if T is 0), may be h0's buffer; h must not alias an input.  ws: its
+ * contents on entry are ignored; calls that may overlap need one each. */
+kdn_status kdn_gated_scan(const kdn_scan_desc *s, const void *x, const void *a, const float *h0,
+                          void *h, float *h_T, void *ws, size_t ws_bytes, void *stream);
+
+/* Its backward: the gradient of <dh, h> + <dh_T, h_T> with respect to x, a and
+ * h0, from the h that the forward left (h as stored: in bfloat16 da carries its
+ * rounding, up to 2^-9 relative).  dh [B,H,T,d] in dtype; dh_T NULL: zeros;
+ * h0 as in the forward.  dx, da [B,H,T,d] and dh0 [B,H,d] (NULL skips it)
+ * float32.  No output may alias an input. */
+kdn_status kdn_gated_scan_backward(const kdn_scan_desc *s, const void *a, const void *h,
+                                   const float *h0, const void *dh, const float *dh_T, float *dx,
+                                   float *da, float *dh0, void *ws, size_t ws_bytes, void *stream);
+
+/* One token in place: x, a, o [B,H,d]; h [B,H,d] float32 is read and
+ * overwritten, and o is its new value in dtype.  s->T is ignored but must not be
+ * negative.  slot NULL, or device int32 [B]: h is then a cache
+ * [n_slots,H,d] and sequence b's state is at slot[b]; outside [0, n_slots) the
+ * sequence is idle (its state and its o row are not touched).  Slots of active
+ * sequences must be distinct (not checked). */
+kdn_status kdn_gated_scan_step(const kdn_scan_desc *s, const void *x, const void *a, float *h,
+                               const int32_t *slot, int32_t n_slots, void *o, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,11 @@ Functions (same names as the C entry points):
   backward(q, k, v, a, qnoise, r, dO, lambda0=None, S0=None, dS_T=None, dlambda_T=None,
            variant="diagonal", chunk=64) -> dict of float32 gradients (dq, dk, dv, da, dqnoise, dr,
            dlambda0, dS0)
+  rms_norm(x, weight, residual=None) -> (y, s, rstd);  rms_norm_quant(...) -> (q, scale, s)
+  rms_norm_backward(dy, s, weight, rstd, ds=None) -> (dx, dweight)
+  quantize(x, block_rows=1) -> (q, scale)      (e4m3, a scale per 1 x 128 or 128 x 128 block)
+  gated_scan(x, a, h0=None) -> (h, h_T);  gated_scan_step(x, a, h, slot=None) -> o
+  gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict of float32 gradients (dx, da, dh0)
 """
 from __future__ import annotations
 
@@ -47,6 +52,10 @@ EXPORTS = (
     "kdn_dense_gain", "kdn_blas_create", "kdn_blas_destroy", "kdn_layer_workspace_bytes",
     "kdn_layer_forward", "kdn_layer_forward_events",
     "kdn_noalloc_scratch_bytes", "kdn_forward_noalloc",
+    "kdn_rms_norm", "kdn_rms_norm_quant", "kdn_rms_norm_backward_workspace_bytes",
+    "kdn_rms_norm_backward", "kdn_quantize",
+    "kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes",
+    "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
 )
 
 
@@ -59,6 +68,20 @@ class KdnDesc(ctypes.Structure):
 class KdnLayerDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "B", "T", "H", "d_model", "d_k", "d_v", "chunk", "variant", "dtype")]
+
+
+class KdnNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class KdnQuantDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("block_rows", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KdnScanDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "T", "d", "dtype", "gate_dtype")]
 
 
 class KdnError(RuntimeError):
@@ -123,6 +146,19 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_noalloc_scratch_bytes.restype = S
     lib.kdn_forward_noalloc.argtypes = [D] + [P] * 11 + [P]
     lib.kdn_forward_noalloc.restype = I
+    N, Q, G = (ctypes.POINTER(t) for t in (KdnNormDesc, KdnQuantDesc, KdnScanDesc))
+    lib.kdn_rms_norm.argtypes = [N] + [P] * 7
+    lib.kdn_rms_norm_quant.argtypes = [N] + [P] * 8
+    lib.kdn_rms_norm_backward_workspace_bytes.argtypes = [N]
+    lib.kdn_rms_norm_backward_workspace_bytes.restype = S
+    lib.kdn_rms_norm_backward.argtypes = [N] + [P] * 8 + [S, P]
+    lib.kdn_quantize.argtypes = [Q] + [P] * 4
+    for n in ("kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes"):
+        getattr(lib, n).argtypes = [G]
+        getattr(lib, n).restype = S
+    lib.kdn_gated_scan.argtypes = [G] + [P] * 6 + [S, P]
+    lib.kdn_gated_scan_backward.argtypes = [G] + [P] * 9 + [S, P]
+    lib.kdn_gated_scan_step.argtypes = [G] + [P] * 4 + [ctypes.c_int32, P, P]
     _lib = lib
     return lib
 
@@ -631,4 +667,198 @@ def decode_step_indexed(q, k, v, a, qnoise, r, S_cache, lam_cache, slot, variant
                                        _ptr(qnoise), _ptr(r), _ptr(S_cache), _ptr(lam_cache),
                                        _ptr(slot), n_slots, _ptr(o), _stream()),
            "kdn_decode_step_indexed")
+    return o
+
+
+def _tensors(*named):
+    """Checks (name, tensor) pairs, None among them: on one GPU, contiguous.
+    Returns that device."""
+    dev = None
+    for name, x in named:
+        if x is None:
+            continue
+        _gpu(x, name)
+        if dev is None:
+            dev = x.device
+        elif x.device != dev:
+            raise ValueError(f"{name} is on {x.device}, the other tensors are on {dev}")
+    return dev
+
+
+def _shaped(name, x, dtype, shape):
+    if x is not None and (x.dtype != dtype or tuple(x.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+
+
+def _launch(name, dev, *args):
+    """A library call with `dev` current and its current torch stream as the last
+    argument."""
+    fn = getattr(load_library(), name)
+    if dev.index == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(code, name)
+
+
+def _norm_desc(x, name, weight, residual_dtype, eps):
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have a last dimension")
+    n = KdnNormDesc()
+    n.d = x.shape[-1]
+    n.rows = x.numel() // n.d if n.d else 0
+    n.dtype = _dtype_code(x.dtype)
+    n.residual_dtype = _dtype_code(residual_dtype)
+    n.eps = eps
+    _shaped("weight", weight, torch.float32, (n.d,))
+    return n
+
+
+def _norm_stream(x, residual, in_place):
+    """The tensor that takes s = x + residual (x itself without a residual)."""
+    if residual is None:
+        return None
+    if residual.shape != x.shape or residual.dtype not in (x.dtype, torch.float32):
+        raise ValueError("residual must have x's shape, and x's dtype or float32")
+    return residual if in_place else torch.empty_like(residual)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, in_place=False):
+    """RMS norm with the residual's addition: s = x + residual (rounded to the
+    residual's dtype; x itself without one), y = s rsqrt(mean(s^2) + eps) weight
+    over the last dimension.  x [..., d] float32 or bfloat16, residual in x's dtype
+    or float32, weight float32 [d].  Returns (y in x's dtype, s, rstd float32
+    [...]).  in_place: s is written over residual."""
+    dev = _tensors(("x", x), ("weight", weight), ("residual", residual))
+    n = _norm_desc(x, "x", weight, x.dtype if residual is None else residual.dtype, eps)
+    s = _norm_stream(x, residual, in_place)
+    y = torch.empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _launch("kdn_rms_norm", dev, ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y),
+            _ptr(s), _ptr(rstd))
+    return y, x if s is None else s, rstd
+
+
+def rms_norm_quant(x, weight, residual=None, eps=1e-6, in_place=False):
+    """rms_norm with y in 8 bits, an operand of quant_matmul.  Returns (q
+    float8_e4m3fn [..., d], scale float32 [..., ceil(d / 128)], s)."""
+    dev = _tensors(("x", x), ("weight", weight), ("residual", residual))
+    n = _norm_desc(x, "x", weight, x.dtype if residual is None else residual.dtype, eps)
+    s = _norm_stream(x, residual, in_place)
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((*x.shape[:-1], -(-n.d // 128)), dtype=torch.float32, device=dev)
+    _launch("kdn_rms_norm_quant", dev, ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(weight),
+            _ptr(q), _ptr(scale), _ptr(s), None)
+    return q, scale, x if s is None else s
+
+
+def rms_norm_backward(dy, s, weight, rstd, ds=None):
+    """Gradient of rms_norm from dy [..., d], the s and rstd it returned, and ds
+    (float32 [..., d] or None), the gradient that reaches s from elsewhere.
+    Returns (dx, dweight), float32: dx is the gradient of s, hence of x and of
+    residual."""
+    dev = _tensors(("dy", dy), ("s", s), ("weight", weight), ("rstd", rstd), ("ds", ds))
+    if s.shape != dy.shape or s.dtype not in (dy.dtype, torch.float32):
+        raise ValueError("s must have dy's shape, and dy's dtype or float32")
+    n = _norm_desc(dy, "dy", weight, s.dtype, 0.0)
+    _shaped("rstd", rstd, torch.float32, dy.shape[:-1])
+    _shaped("ds", ds, torch.float32, dy.shape)
+    need = load_library().kdn_rms_norm_backward_workspace_bytes(ctypes.byref(n))
+    dx = torch.empty(dy.shape, dtype=torch.float32, device=dev)
+    dw = torch.empty(n.d, dtype=torch.float32, device=dev)
+    ws = _workspace(need, dev)
+    _launch("kdn_rms_norm_backward", dev, ctypes.byref(n), _ptr(dy), _ptr(s), _ptr(weight),
+            _ptr(rstd), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel())
+    return dx, dw
+
+
+def quantize(x, block_rows=1):
+    """x [..., d] float32 or bfloat16 in 8 bits: (q float8_e4m3fn [..., d], scale
+    float32).  block_rows 1 (activations): a scale per 128 columns of a row,
+    [..., ceil(d / 128)]; 128 (weights, x [rows, d]): per 128 x 128 block,
+    [ceil(rows / 128), ceil(d / 128)]."""
+    dev = _tensors(("x", x))
+    if x.dim() == 0 or (block_rows != 1 and x.dim() != 2):
+        raise ValueError("x must be [..., d], and [rows, d] for blocks of several rows")
+    n = KdnQuantDesc()
+    n.d = x.shape[-1]
+    n.rows = x.numel() // n.d if n.d else 0
+    n.block_rows = block_rows
+    n.dtype = _dtype_code(x.dtype)
+    nb = -(-n.d // 128)
+    lead = x.shape[:-1] if block_rows == 1 else (-(-x.shape[0] // max(1, block_rows)),)
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    scale = torch.empty((*lead, nb), dtype=torch.float32, device=dev)
+    _launch("kdn_quantize", dev, ctypes.byref(n), _ptr(x), _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def make_scan_desc(B, H, T, d, dtype, gate_dtype) -> KdnScanDesc:
+    s = KdnScanDesc()
+    s.B, s.H, s.T, s.d, s.dtype, s.gate_dtype = B, H, T, d, dtype, gate_dtype
+    return s
+
+
+def gated_scan(x, a, h0=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + x_t per channel: x, a
+    [B,H,T,d] (float32 or bfloat16 each), h0 float32 [B,H,d] or None (zeros).
+    Returns (h in x's dtype [B,H,T,d], h_T float32 [B,H,d])."""
+    dev = _tensors(("x", x), ("a", a), ("h0", h0))
+    if x.dim() != 4 or a.shape != x.shape:
+        raise ValueError("x and a must be [B,H,T,d]")
+    B, H, T, d = x.shape
+    _shaped("h0", h0, torch.float32, (B, H, d))
+    s = make_scan_desc(B, H, T, d, _dtype_code(x.dtype), _dtype_code(a.dtype))
+    need = load_library().kdn_gated_scan_workspace_bytes(ctypes.byref(s))
+    h = torch.empty_like(x)
+    h_T = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+    ws = _workspace(need, dev)
+    _launch("kdn_gated_scan", dev, ctypes.byref(s), _ptr(x), _ptr(a), _ptr(h0), _ptr(h),
+            _ptr(h_T), _ptr(ws), ws.numel())
+    return h, h_T
+
+
+def gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict:
+    """Gradients of <dh, h> + <dh_T, h_T> with respect to x, a and h0 of
+    gated_scan, from a, the h it returned, dh (h's dtype) and dh_T (float32
+    [B,H,d] or None), as float32 tensors in a dict (keys dx, da, dh0)."""
+    dev = _tensors(("a", a), ("h", h), ("dh", dh), ("h0", h0), ("dh_T", dh_T))
+    if h.dim() != 4 or a.shape != h.shape:
+        raise ValueError("a and h must be [B,H,T,d]")
+    B, H, T, d = h.shape
+    _shaped("dh", dh, h.dtype, h.shape)
+    _shaped("h0", h0, torch.float32, (B, H, d))
+    _shaped("dh_T", dh_T, torch.float32, (B, H, d))
+    s = make_scan_desc(B, H, T, d, _dtype_code(h.dtype), _dtype_code(a.dtype))
+    need = load_library().kdn_gated_scan_backward_workspace_bytes(ctypes.byref(s))
+    g = {n: torch.empty(h.shape, dtype=torch.float32, device=dev) for n in ("dx", "da")}
+    g["dh0"] = torch.empty((B, H, d), dtype=torch.float32, device=dev)
+    ws = _workspace(need, dev)
+    _launch("kdn_gated_scan_backward", dev, ctypes.byref(s), _ptr(a), _ptr(h), _ptr(h0), _ptr(dh),
+            _ptr(dh_T), _ptr(g["dx"]), _ptr(g["da"]), _ptr(g["dh0"]), _ptr(ws), ws.numel())
+    return g
+
+
+def gated_scan_step(x, a, h, slot=None, out=None):
+    """One token of gated_scan in place: x, a [B,H,d]; h float32 [B,H,d] is
+    overwritten with the new state.  slot: int32 [B] on the GPU; h is then a cache
+    [n_slots,H,d] and sequence b's state is at slot[b] (outside [0, n_slots):
+    idle; slots of active sequences must be distinct).  Returns o [B,H,d], the new
+    state in x's dtype (rows of idle sequences are left as they were in `out`, or
+    uninitialised)."""
+    dev = _tensors(("x", x), ("a", a), ("h", h), ("slot", slot), ("out", out))
+    if x.dim() != 3 or a.shape != x.shape:
+        raise ValueError("x and a must be [B,H,d]")
+    B, H, d = x.shape
+    if h.dim() != 3:
+        raise ValueError("h must be [B,H,d], or [n_slots,H,d] with slot")
+    n_slots = h.shape[0]
+    _shaped("h", h, torch.float32, (B if slot is None else n_slots, H, d))
+    _shaped("slot", slot, torch.int32, (B,))
+    _shaped("out", out, x.dtype, x.shape)
+    s = make_scan_desc(B, H, 1, d, _dtype_code(x.dtype), _dtype_code(a.dtype))
+    o = out if out is not None else torch.empty_like(x)
+    _launch("kdn_gated_scan_step", dev, ctypes.byref(s), _ptr(x), _ptr(a), _ptr(h), _ptr(slot),
+            n_slots, _ptr(o))
     return o
