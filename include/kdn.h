@@ -468,6 +468,22 @@ typedef struct {
 kdn_status kdn_quantize(const kdn_quant_desc *n, const void *x, void *q, float *scale,
                         void *stream);
 
+/* C = A B^T of 8-bit operands:
+ *   C[m][n] = sum_kb sA[m][kb] sB[n / 128][kb] sum_{k in block kb} A[m][k] B[n][k]
+ * A [M, K] with sA [M, ceil(K / 128)] (kdn_quantize with block_rows 1, or
+ * kdn_rms_norm_quant), B [N, K] with sB [ceil(N / 128), ceil(K / 128)]
+ * (block_rows 128), C [M, N] in dtype with rows ldc >= N elements apart (what
+ * lies behind the N columns of a row is not written).  Sums are float32, rounded
+ * once into C.  K a multiple of 16 (0: C is zero) up to 2^23, the other sizes up to
+ * 2^28, and fewer than 2^22 tiles of 64 x 64 of C (KDN_ERR_UNSUPPORTED otherwise).  A, B and C
+ * 16-byte aligned; C must not alias an input. */
+typedef struct {
+    int32_t M, N, K, ldc;
+    int32_t dtype; /* kdn_dtype of C */
+} kdn_gemm_desc;
+kdn_status kdn_quant_gemm(const kdn_gemm_desc *d, const void *A, const float *sA, const void *B,
+                          const float *sB, void *C, void *stream);
+
 /* ------------------------------------------------------- gated recurrence
  * The linear recurrence without a key space, h_t = a_t h_{t-1} + x_t for each
  * channel, as it is stacked with KDN layers: the token maps h -> a h + x compose

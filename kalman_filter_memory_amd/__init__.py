@@ -24,6 +24,7 @@ Functions (same names as the C entry points):
   rms_norm(x, weight, residual=None) -> (y, s, rstd);  rms_norm_quant(...) -> (q, scale, s)
   rms_norm_backward(dy, s, weight, rstd, ds=None) -> (dx, dweight)
   quantize(x, block_rows=1) -> (q, scale)      (e4m3, a scale per 1 x 128 or 128 x 128 block)
+  quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16) -> a b^T of 8-bit operands
   gated_scan(x, a, h0=None) -> (h, h_T);  gated_scan_step(x, a, h, slot=None) -> o
   gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict of float32 gradients (dx, da, dh0)
 """
@@ -53,7 +54,7 @@ EXPORTS = (
     "kdn_layer_forward", "kdn_layer_forward_events",
     "kdn_noalloc_scratch_bytes", "kdn_forward_noalloc",
     "kdn_rms_norm", "kdn_rms_norm_quant", "kdn_rms_norm_backward_workspace_bytes",
-    "kdn_rms_norm_backward", "kdn_quantize",
+    "kdn_rms_norm_backward", "kdn_quantize", "kdn_quant_gemm",
     "kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes",
     "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
 )
@@ -78,6 +79,10 @@ class KdnNormDesc(ctypes.Structure):
 class KdnQuantDesc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("block_rows", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class KdnGemmDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "ldc", "dtype")]
 
 
 class KdnScanDesc(ctypes.Structure):
@@ -153,6 +158,7 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_rms_norm_backward_workspace_bytes.restype = S
     lib.kdn_rms_norm_backward.argtypes = [N] + [P] * 8 + [S, P]
     lib.kdn_quantize.argtypes = [Q] + [P] * 4
+    lib.kdn_quant_gemm.argtypes = [ctypes.POINTER(KdnGemmDesc)] + [P] * 6
     for n in ("kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes"):
         getattr(lib, n).argtypes = [G]
         getattr(lib, n).restype = S
@@ -792,6 +798,31 @@ def quantize(x, block_rows=1):
     scale = torch.empty((*lead, nb), dtype=torch.float32, device=dev)
     _launch("kdn_quantize", dev, ctypes.byref(n), _ptr(x), _ptr(q), _ptr(scale))
     return q, scale
+
+
+def quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
+    """a b^T of 8-bit operands with a scale for each block of 128: a
+    float8_e4m3fn [..., K] with a_scale [..., ceil(K / 128)] (quantize or
+    rms_norm_quant), b float8_e4m3fn [N, K] with b_scale [ceil(N / 128),
+    ceil(K / 128)] (quantize with block_rows=128).  Returns [..., N] in out_dtype
+    (float32 or bfloat16); sums are float32."""
+    dev = _tensors(("a", a), ("a_scale", a_scale), ("b", b), ("b_scale", b_scale))
+    if a.dtype != torch.float8_e4m3fn or b.dtype != torch.float8_e4m3fn:
+        raise TypeError("a and b must be float8_e4m3fn")
+    if a.dim() == 0 or b.dim() != 2 or a.shape[-1] != b.shape[1]:
+        raise ValueError("a must be [..., K] and b [N, K]")
+    N, K = b.shape
+    lead = a.shape[:-1]
+    kb = -(-K // 128)
+    _shaped("a_scale", a_scale, torch.float32, (*lead, kb))
+    _shaped("b_scale", b_scale, torch.float32, (-(-N // 128), kb))
+    d = KdnGemmDesc()
+    d.M, d.N, d.K, d.ldc = lead.numel(), N, K, N
+    d.dtype = _dtype_code(out_dtype)
+    c = torch.empty((*lead, N), dtype=out_dtype, device=dev)
+    _launch("kdn_quant_gemm", dev, ctypes.byref(d), _ptr(a), _ptr(a_scale), _ptr(b),
+            _ptr(b_scale), _ptr(c))
+    return c
 
 
 def make_scan_desc(B, H, T, d, dtype, gate_dtype) -> KdnScanDesc:

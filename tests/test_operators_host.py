@@ -172,3 +172,36 @@ def test_binding_refuses_cpu_tensors(lib):
                  lambda: kdn.gated_scan_step(y[0], y[0], y[0])):
         with pytest.raises(kdn.KdnError):
             call()
+
+
+GEMM_BAD = [
+    (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=-16), 2), (dict(ldc=199), 2), (dict(K=24), 3),
+    (dict(dtype=2), 3), (dict(K=(1 << 23) + 16), 3), (dict(M=(1 << 28) + 1), 3),
+    (dict(M=1 << 20, N=1 << 20, ldc=1 << 20), 3),
+]
+
+
+def _gemm(M=20, N=200, K=256, ldc=200, dtype=kdn.BF16):
+    d = kdn.KdnGemmDesc()
+    d.M, d.N, d.K, d.ldc, d.dtype = M, N, K, ldc, dtype
+    return d
+
+
+@pytest.mark.parametrize("kw,code", GEMM_BAD, ids=[str(k) for k, _ in GEMM_BAD])
+def test_quant_gemm_refuses_descriptors(lib, kw, code):
+    assert lib.kdn_quant_gemm(ctypes.byref(_gemm(**kw)), *([FAKE] * 5), None) == code
+
+
+def test_quant_gemm_refuses_arguments(lib):
+    d = ctypes.byref(_gemm())
+    assert lib.kdn_quant_gemm(None, *([FAKE] * 5), None) == 1
+    for i in range(5):
+        args = [FAKE] * 5
+        args[i] = None
+        assert lib.kdn_quant_gemm(d, *args, None) == 1
+    for i in (0, 2, 4):
+        args = [FAKE] * 5
+        args[i] = ODD
+        assert lib.kdn_quant_gemm(d, *args, None) == 5
+    assert lib.kdn_quant_gemm(ctypes.byref(_gemm(M=0)), *([None] * 5), None) == 0
+    assert lib.kdn_quant_gemm(ctypes.byref(_gemm(N=0)), *([None] * 5), None) == 0
