@@ -484,6 +484,30 @@ typedef struct {
 kdn_status kdn_quant_gemm(const kdn_gemm_desc *d, const void *A, const float *sA, const void *B,
                           const float *sB, void *C, void *stream);
 
+/* ------------------------------------------------------- layer in 8 bits
+ * The layer as a pre-norm block with 8-bit projections, on the operators above:
+ *   s = x + residual (kdn_rms_norm_quant: the residual stream, and its norm in
+ *       8 bits; residual NULL: s is x and not written)
+ *   Z = norm(s) W_in^T, q, k, v, gates and recurrence as in kdn_layer_forward
+ *   y = [o_1 .. o_H] W_out^T, with the read-out quantised per 128 columns.
+ * W_in and W_out are e4m3 with a scale per 128 x 128 block (kdn_quantize,
+ * block_rows 128), laid out as in kdn_layer_forward; norm_weight [d_model] and
+ * b_gate [3H] float32; x, Z, the recurrence and y in d->dtype; residual and s in
+ * residual_dtype (KDN_F32 or dtype).  The caller adds y to s, or hands both to
+ * the next block as x and residual.  Limits: kdn_layer_forward's, d_model a
+ * multiple of 16, and those of the operators (KDN_ERR_UNSUPPORTED otherwise;
+ * the workspace query returns 0).  s may be residual's buffer and S_T, lambda_T
+ * those of S0, lambda0; y must not alias an input.  No library context: every
+ * kernel is this library's. */
+size_t kdn_layer_quant_workspace_bytes(const kdn_layer_desc *d);
+kdn_status kdn_layer_quant_forward(const kdn_layer_desc *d, const void *x, const void *residual,
+                                   int32_t residual_dtype, const float *norm_weight, float eps,
+                                   const void *W_in, const float *W_in_scale, const float *b_gate,
+                                   const void *W_out, const float *W_out_scale,
+                                   const float *lambda0, const float *S0, void *y, void *s,
+                                   float *S_T, float *lambda_T, void *ws, size_t ws_bytes,
+                                   void *stream);
+
 /* ------------------------------------------------------- gated recurrence
  * The linear recurrence without a key space, h_t = a_t h_{t-1} + x_t for each
  * channel, as it is stacked with KDN layers: the token maps h -> a h + x compose

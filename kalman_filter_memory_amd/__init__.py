@@ -25,6 +25,8 @@ Functions (same names as the C entry points):
   rms_norm_backward(dy, s, weight, rstd, ds=None) -> (dx, dweight)
   quantize(x, block_rows=1) -> (q, scale)      (e4m3, a scale per 1 x 128 or 128 x 128 block)
   quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16) -> a b^T of 8-bit operands
+  layer_quant_forward(x, norm_weight, W_in, W_in_scale, b_gate, W_out, W_out_scale, H, d_k, d_v,
+                      residual=None, ...) -> (y, s, S_T, lambda_T)   (the layer in 8 bits)
   gated_scan(x, a, h0=None) -> (h, h_T);  gated_scan_step(x, a, h, slot=None) -> o
   gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict of float32 gradients (dx, da, dh0)
 """
@@ -55,6 +57,7 @@ EXPORTS = (
     "kdn_noalloc_scratch_bytes", "kdn_forward_noalloc",
     "kdn_rms_norm", "kdn_rms_norm_quant", "kdn_rms_norm_backward_workspace_bytes",
     "kdn_rms_norm_backward", "kdn_quantize", "kdn_quant_gemm",
+    "kdn_layer_quant_workspace_bytes", "kdn_layer_quant_forward",
     "kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes",
     "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
 )
@@ -159,6 +162,10 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_rms_norm_backward.argtypes = [N] + [P] * 8 + [S, P]
     lib.kdn_quantize.argtypes = [Q] + [P] * 4
     lib.kdn_quant_gemm.argtypes = [ctypes.POINTER(KdnGemmDesc)] + [P] * 6
+    lib.kdn_layer_quant_workspace_bytes.argtypes = [L]
+    lib.kdn_layer_quant_workspace_bytes.restype = S
+    lib.kdn_layer_quant_forward.argtypes = ([L, P, P, ctypes.c_int32, P, ctypes.c_float]
+                                            + [P] * 12 + [S, P])
     for n in ("kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes"):
         getattr(lib, n).argtypes = [G]
         getattr(lib, n).restype = S
@@ -823,6 +830,54 @@ def quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     _launch("kdn_quant_gemm", dev, ctypes.byref(d), _ptr(a), _ptr(a_scale), _ptr(b),
             _ptr(b_scale), _ptr(c))
     return c
+
+
+def layer_quant_workspace_bytes(d: KdnLayerDesc) -> int:
+    return int(load_library().kdn_layer_quant_workspace_bytes(ctypes.byref(d)))
+
+
+def layer_quant_forward(x, norm_weight, W_in, W_in_scale, b_gate, W_out, W_out_scale, H, d_k, d_v,
+                        residual=None, eps=1e-6, lambda0=None, S0=None, variant="diagonal",
+                        chunk=64, workspace=None, in_place=False):
+    """The KDN layer as a pre-norm block with 8-bit projections: s = x + residual,
+    y = layer(rms_norm(s) norm_weight).  x [B,T,D] float32 or bfloat16; residual
+    None or [B,T,D] in x's dtype or float32 (in_place: s is written over it);
+    W_in [H(2 d_k + d_v) + 3H, D] and W_out [D, H d_v] float8_e4m3fn with their
+    scales (quantize with block_rows=128); norm_weight [D] and b_gate [3H] float32.
+    Returns (y in x's dtype, s, S_T, lambda_T)."""
+    dev = _tensors(("x", x), ("norm_weight", norm_weight), ("W_in", W_in),
+                   ("W_in_scale", W_in_scale), ("b_gate", b_gate), ("W_out", W_out),
+                   ("W_out_scale", W_out_scale), ("residual", residual), ("lambda0", lambda0),
+                   ("S0", S0), ("workspace", workspace))
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,D]")
+    B, T, D = x.shape
+    n_in, n_out = H * (2 * d_k + d_v) + 3 * H, H * d_v
+    f32, fp8 = torch.float32, torch.float8_e4m3fn
+    _shaped("norm_weight", norm_weight, f32, (D,))
+    _shaped("W_in", W_in, fp8, (n_in, D))
+    _shaped("W_in_scale", W_in_scale, f32, (-(-n_in // 128), -(-D // 128)))
+    _shaped("b_gate", b_gate, f32, (3 * H,))
+    _shaped("W_out", W_out, fp8, (D, n_out))
+    _shaped("W_out_scale", W_out_scale, f32, (-(-D // 128), -(-n_out // 128)))
+    d = make_layer_desc(B, T, H, D, d_k, d_v, chunk, variant, _dtype_code(x.dtype))
+    lam_shape = (B, H, d_k) if d.variant == DIAGONAL else (B, H)
+    _shaped("lambda0", lambda0, f32, lam_shape)
+    _shaped("S0", S0, f32, (B, H, d_v, d_k))
+    need = layer_quant_workspace_bytes(d)
+    if need == 0:
+        raise KdnError("kdn_layer_quant_forward: unsupported layer shape")
+    s = _norm_stream(x, residual, in_place)
+    ws = workspace if workspace is not None else _workspace(need, dev)
+    y = torch.empty_like(x)
+    S_T = torch.empty((B, H, d_v, d_k), dtype=f32, device=dev)
+    lam_T = torch.empty(lam_shape, dtype=f32, device=dev)
+    _launch("kdn_layer_quant_forward", dev, ctypes.byref(d), _ptr(x), _ptr(residual),
+            d.dtype if residual is None else _dtype_code(residual.dtype), _ptr(norm_weight), eps,
+            _ptr(W_in), _ptr(W_in_scale), _ptr(b_gate), _ptr(W_out), _ptr(W_out_scale),
+            _ptr(lambda0), _ptr(S0), _ptr(y), _ptr(s), _ptr(S_T), _ptr(lam_T), _ptr(ws),
+            ws.numel() * ws.element_size())
+    return y, x if s is None else s, S_T, lam_T
 
 
 def make_scan_desc(B, H, T, d, dtype, gate_dtype) -> KdnScanDesc:

@@ -19,6 +19,11 @@
 // [B, H, T, .] are one pass (layer_in_kernel); the read-out goes back to token
 // rows in another (layer_out_kernel).  Both are HBM-bound copies with 16-byte
 // accesses.
+//
+// kdn_layer_quant_forward is the layer as a pre-norm block whose projections run in
+// 8 bits: the norm with the residual's addition writes the input product's 8-bit
+// operand, and the read-out goes to token rows in 8 bits in one pass
+// (layer_out_quant_kernel), so neither operand exists in 16 bits.
 #include <hipblaslt/hipblaslt.h>
 
 #include <algorithm>
@@ -26,7 +31,7 @@
 #include <new>
 
 #include "kdn.h"
-#include "kdn_device.h"
+#include "kdn_quant.h"
 
 namespace {
 
@@ -186,6 +191,32 @@ __global__ __launch_bounds__(256) void layer_out_kernel(const E* __restrict__ o,
     }
 }
 
+// o [B,H,T,DV] -> token rows [B*T, H*DV] in 8 bits with a scale per 128 columns: 16
+// lanes per block of 128, as in the quantiser, one workgroup per token row
+template <typename E, int DV>
+__global__ __launch_bounds__(256) void layer_out_quant_kernel(const E* __restrict__ o,
+                                                              uint8_t* __restrict__ q,
+                                                              float* __restrict__ scale, int H,
+                                                              int T) {
+    const int row = blockIdx.x, b = row / T, t = row % T, n = H * DV;
+    const int l16 = threadIdx.x & 15, nb = (n + kdn::kQuantBlock - 1) / kdn::kQuantBlock;
+    // (the 16 lanes of a block leave the loop together)
+    for (int blk = threadIdx.x >> 4; blk < nb; blk += 16) {
+        const int c = kdn::kQuantBlock * blk + 8 * l16, h = c / DV, j = c % DV;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+        if (c < n) kdn::load_vec<E, 8>(o + ((size_t(b) * H + h) * T + t) * DV + j, f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = kdn::umax(m, kdn::abs_bits(f[i]));
+        const float sc = kdn::quant_scale(kdn::row_umax(m));
+        if (c < n)
+            *reinterpret_cast<kdn::u32x2*>(q + size_t(row) * n + c) = kdn::quant8(f, 1.f / sc);
+        if (l16 == 0) scale[size_t(row) * nb + blk] = sc;
+    }
+}
+
 template <typename E, int DK, int DV>
 hipError_t in_t(const void* Z, int ldz, const float* bg, int M, int H, int T, void* q, void* k,
                 void* v, void* a, void* nu, void* r, hipStream_t st) {
@@ -217,6 +248,20 @@ hipError_t launch_out(int dv, const void* o, void* o2, int M, int H, int T, hipS
     }
     KDN_LAYER_OUT(32) KDN_LAYER_OUT(64) KDN_LAYER_OUT(128)
 #undef KDN_LAYER_OUT
+    return hipErrorInvalidValue;
+}
+
+template <typename E>
+hipError_t launch_out_quant(int dv, const void* o, void* q, float* scale, int M, int H, int T,
+                            hipStream_t st) {
+#define KDN_LAYER_OUT_QUANT(DV_)                                                              \
+    if (dv == DV_) {                                                                          \
+        layer_out_quant_kernel<E, DV_><<<M, 256, 0, st>>>(                                    \
+            static_cast<const E*>(o), static_cast<uint8_t*>(q), scale, H, T);                 \
+        return hipGetLastError();                                                             \
+    }
+    KDN_LAYER_OUT_QUANT(32) KDN_LAYER_OUT_QUANT(64) KDN_LAYER_OUT_QUANT(128)
+#undef KDN_LAYER_OUT_QUANT
     return hipErrorInvalidValue;
 }
 
@@ -271,6 +316,53 @@ LayerWs layer_ws(const kdn_layer_desc* d) {
     return w;
 }
 
+// The workspace of the layer in 8 bits: as above, with the 8-bit operand of the
+// two products (one after the other) in place of the library's workspace.
+struct QuantLayerWs {
+    size_t z, x8, scale, q, k, v, a, nu, r, o, core, total;
+    int ldz;
+};
+
+int blocks128(int n) { return (n + kdn::kQuantBlock - 1) / kdn::kQuantBlock; }
+
+QuantLayerWs quant_layer_ws(const kdn_layer_desc* d) {
+    const size_t es = d->dtype == KDN_BF16 ? 2 : 4;
+    const size_t M = size_t(d->B) * d->T, BH = size_t(d->B) * d->H;
+    QuantLayerWs w{};
+    w.ldz = (n_in(d) + 63) / 64 * 64;  // rows of Z start on a cache line
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += align256(bytes);
+        return o;
+    };
+    const int width = std::max(d->d_model, d->H * d->d_v);
+    w.z = take(M * w.ldz * es);
+    w.x8 = take(M * width);
+    w.scale = take(M * blocks128(width) * 4);
+    w.q = take(BH * d->T * d->d_k * es);
+    w.k = take(BH * d->T * d->d_k * es);
+    w.v = take(BH * d->T * d->d_v * es);
+    w.a = take(BH * d->T * es);
+    w.nu = take(BH * d->T * es);
+    w.r = take(BH * d->T * es);
+    w.o = take(BH * d->T * d->d_v * es);
+    const kdn_desc c = core_desc(d);
+    w.core = take(kdn_forward_workspace_bytes(&c));
+    w.total = off;
+    return w;
+}
+
+kdn_gemm_desc gemm_desc(int M, int N, int K, int ldc, int dtype) {
+    kdn_gemm_desc g{};
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.ldc = ldc;
+    g.dtype = dtype;
+    return g;
+}
+
 kdn_status check_layer(const kdn_layer_desc* d) {
     if (!d) return KDN_ERR_NULL;
     if (d->B < 0 || d->T < 0 || d->H < 0 || d->d_model < 0) return KDN_ERR_SHAPE;
@@ -283,6 +375,25 @@ kdn_status check_layer(const kdn_layer_desc* d) {
     if (int64_t(d->H) * (2 * d->d_k + d->d_v + 3) > INT32_MAX / 16) return KDN_ERR_UNSUPPORTED;
     const kdn_desc c = core_desc(d);
     return kdn_validate(&c);
+}
+
+// the layer's checks, and those of the calls the layer in 8 bits is made of (which
+// look at their descriptors before their pointers: KDN_ERR_NULL means that they
+// take it)
+kdn_status check_quant_layer(const kdn_layer_desc* d, int residual_dtype, float eps) {
+    const kdn_status st = check_layer(d);
+    if (st != KDN_OK) return st;
+    const int64_t M = int64_t(d->B) * d->T;
+    const kdn_norm_desc n{M, d->d_model, d->dtype, residual_dtype, eps};
+    const int width = d->H * d->d_v;
+    const kdn_gemm_desc in = gemm_desc(int(M), n_in(d), d->d_model, (n_in(d) + 63) / 64 * 64, d->dtype);
+    const kdn_gemm_desc out = gemm_desc(int(M), d->d_model, width, d->d_model, d->dtype);
+    for (const kdn_status s :
+         {kdn_rms_norm_quant(&n, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr),
+          kdn_quant_gemm(&in, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr),
+          kdn_quant_gemm(&out, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr)})
+        if (s != KDN_OK && s != KDN_ERR_NULL) return s;
+    return KDN_OK;
 }
 
 char* at(void* base, size_t off) { return static_cast<char*>(base) + off; }
@@ -410,6 +521,34 @@ kdn_status layer_forward_t(const kdn_layer_desc* d, BlasCtx* hb, const void* x,
     return KDN_OK;
 }
 
+template <typename E>
+kdn_status layer_quant_t(const kdn_layer_desc* d, const kdn_norm_desc& n, const void* x,
+                         const void* residual, const float* norm_weight, const void* W_in,
+                         const float* W_in_scale, const float* b_gate, const void* W_out,
+                         const float* W_out_scale, const float* lambda0, const float* S0, void* y,
+                         void* s, float* S_T, float* lambda_T, void* ws, const QuantLayerWs& w,
+                         hipStream_t st) {
+    const int M = d->B * d->T, H = d->H, D = d->d_model, dv = d->d_v;
+    void *Z = at(ws, w.z), *x8 = at(ws, w.x8), *o = at(ws, w.o);
+    float* scale = reinterpret_cast<float*>(at(ws, w.scale));
+    void *q = at(ws, w.q), *k = at(ws, w.k), *v = at(ws, w.v);
+    void *a = at(ws, w.a), *nu = at(ws, w.nu), *r = at(ws, w.r);
+    kdn_status e = kdn_rms_norm_quant(&n, x, residual, norm_weight, x8, scale, s, nullptr, st);
+    if (e != KDN_OK) return e;
+    const kdn_gemm_desc in = gemm_desc(M, n_in(d), D, w.ldz, d->dtype);
+    e = kdn_quant_gemm(&in, x8, scale, W_in, W_in_scale, Z, st);
+    if (e != KDN_OK) return e;
+    if (launch_in<E>(d->d_k, dv, Z, w.ldz, b_gate, M, H, d->T, q, k, v, a, nu, r, st) != hipSuccess)
+        return KDN_ERR_HIP;
+    const kdn_desc c = core_desc(d);
+    e = kdn_forward(&c, q, k, v, a, nu, r, lambda0, S0, o, S_T, lambda_T, at(ws, w.core),
+                    w.total - w.core, st);
+    if (e != KDN_OK) return e;
+    if (launch_out_quant<E>(dv, o, x8, scale, M, H, d->T, st) != hipSuccess) return KDN_ERR_HIP;
+    const kdn_gemm_desc out = gemm_desc(M, D, H * dv, D, d->dtype);
+    return kdn_quant_gemm(&out, x8, scale, W_out, W_out_scale, y, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -476,6 +615,45 @@ kdn_status kdn_layer_forward(const kdn_layer_desc* d, void* blas, const void* x,
                              size_t ws_bytes, void* stream) {
     return kdn_layer_forward_events(d, blas, x, W_in, b_gate, W_out, lambda0, S0, y, S_T,
                                     lambda_T, ws, ws_bytes, stream, nullptr);
+}
+
+size_t kdn_layer_quant_workspace_bytes(const kdn_layer_desc* d) {
+    if (check_quant_layer(d, KDN_F32, 0.f) != KDN_OK) return 0;
+    return quant_layer_ws(d).total;
+}
+
+kdn_status kdn_layer_quant_forward(const kdn_layer_desc* d, const void* x, const void* residual,
+                                   int32_t residual_dtype, const float* norm_weight, float eps,
+                                   const void* W_in, const float* W_in_scale, const float* b_gate,
+                                   const void* W_out, const float* W_out_scale,
+                                   const float* lambda0, const float* S0, void* y, void* s,
+                                   float* S_T, float* lambda_T, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    const kdn_status st = check_quant_layer(d, residual_dtype, eps);
+    if (st != KDN_OK) return st;
+    if (d->B == 0 || d->H == 0) return KDN_OK;
+    if (!ws) return KDN_ERR_NULL;
+    const QuantLayerWs w = quant_layer_ws(d);
+    if (d->T == 0) {  // no token rows: only the state passes through
+        if (ws_bytes < w.total) return KDN_ERR_WORKSPACE;
+        const kdn_desc c = core_desc(d);
+        return kdn_forward(&c, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, lambda0, S0,
+                           nullptr, S_T, lambda_T, at(ws, w.core), w.total - w.core, stream);
+    }
+    if (!x || !norm_weight || !W_in || !W_in_scale || !b_gate || !W_out || !W_out_scale || !y)
+        return KDN_ERR_NULL;
+    if ((residual != nullptr) != (s != nullptr)) return KDN_ERR_NULL;
+    if (ws_bytes < w.total) return KDN_ERR_WORKSPACE;
+    for (const void* p : {x, residual, (const void*)norm_weight, W_in, W_out, (const void*)y,
+                          (const void*)s, (const void*)ws})
+        if (!aligned16(p)) return KDN_ERR_ALIGN;
+    const kdn_norm_desc n{int64_t(d->B) * d->T, d->d_model, d->dtype, residual_dtype, eps};
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    return d->dtype == KDN_BF16
+               ? layer_quant_t<bf16_t>(d, n, x, residual, norm_weight, W_in, W_in_scale, b_gate,
+                                       W_out, W_out_scale, lambda0, S0, y, s, S_T, lambda_T, ws, w, hs)
+               : layer_quant_t<float>(d, n, x, residual, norm_weight, W_in, W_in_scale, b_gate,
+                                      W_out, W_out_scale, lambda0, S0, y, s, S_T, lambda_T, ws, w, hs);
 }
 
 }  // extern "C"

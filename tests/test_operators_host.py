@@ -205,3 +205,35 @@ def test_quant_gemm_refuses_arguments(lib):
         assert lib.kdn_quant_gemm(d, *args, None) == 5
     assert lib.kdn_quant_gemm(ctypes.byref(_gemm(M=0)), *([None] * 5), None) == 0
     assert lib.kdn_quant_gemm(ctypes.byref(_gemm(N=0)), *([None] * 5), None) == 0
+
+
+def test_layer_in_8_bits_host_side_checks(lib):
+    def desc(B=1, T=16, H=2, D=64, dk=32, dv=32, chunk=16, dtype=kdn.F32):
+        return kdn.make_layer_desc(B, T, H, D, dk, dv, chunk, "diagonal", dtype)
+
+    d = desc()
+    need = kdn.layer_quant_workspace_bytes(d)
+    core = kdn.forward_workspace_bytes(kdn.make_desc(1, 2, 16, 32, 32, 16, "diagonal", kdn.F32, kdn.F32))
+    # Z (198 columns in rows of 256), 8 bits and scales, q k v o, three gates
+    expect = 16 * 256 * 4 + 16 * 64 + 16 * 4 + 4 * 2 * 16 * 32 * 4 + 3 * 2 * 16 * 4 + core
+    assert expect <= need <= expect + 11 * 256
+    for kw in (dict(D=40), dict(D=16400), dict(dk=48), dict(H=90), dict(dtype=7), dict(B=1 << 15, T=1 << 15)):
+        assert kdn.layer_quant_workspace_bytes(desc(**kw)) == 0, kw
+    call = lib.kdn_layer_quant_forward
+
+    def args(**kw):
+        a = dict(x=FAKE, residual=FAKE, rd=kdn.F32, nw=FAKE, eps=1e-6, wi=FAKE, wis=FAKE, bg=FAKE, wo=FAKE,
+                 wos=FAKE, l0=None, s0=None, y=FAKE, s=FAKE, st=None, lt=None, ws=FAKE, n=need, stream=None)
+        a.update(kw)
+        return list(a.values())
+
+    assert call(None, *args()) == 1
+    for n in ("x", "nw", "wi", "wis", "bg", "wo", "wos", "y", "s", "residual", "ws"):
+        assert call(ctypes.byref(d), *args(**{n: None})) == 1, n
+    for n in ("x", "residual", "nw", "wi", "wo", "y", "s", "ws"):
+        assert call(ctypes.byref(d), *args(**{n: ODD})) == 5, n
+    assert call(ctypes.byref(d), *args(n=need - 1)) == 4
+    assert call(ctypes.byref(d), *args(eps=-1.0)) == 2
+    assert call(ctypes.byref(d), *args(rd=kdn.BF16)) == 3
+    assert call(ctypes.byref(desc(D=40)), *args()) == 3
+    assert call(ctypes.byref(desc(B=0)), *([None] * 2), kdn.F32, None, 1e-6, *([None] * 12), 0, None) == 0
