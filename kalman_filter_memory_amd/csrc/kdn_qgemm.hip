@@ -27,6 +27,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kdn.h"
 #include "kdn_quant.h"
@@ -53,13 +54,17 @@ struct GemmArgs {
     int mt, nt;
 };
 
-// A lane's 32 bytes of a row of one block, and the product of 16 rows by 16 rows
+// a lane's 32 bytes of a row of one block
+struct Raw {
+    u32x4 lo, hi;
+};
+// the same as the instruction takes them, and the product of 16 rows by 16 rows
 template <typename Eo> struct Block;
 template <> struct Block<bf16_t> {
     v8i x;
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
-        x = v8i{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
-                int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    __device__ __forceinline__ void set(const Raw& r) {
+        x = v8i{int(r.lo[0]), int(r.lo[1]), int(r.lo[2]), int(r.lo[3]),
+                int(r.hi[0]), int(r.hi[1]), int(r.hi[2]), int(r.hi[3])};
     }
     static __device__ __forceinline__ floatx4 mul(const Block& a, const Block& b) {
         const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -68,11 +73,11 @@ template <> struct Block<bf16_t> {
 };
 template <> struct Block<float> {
     kdn::bf16x8 x[4];
-    __device__ __forceinline__ void set(u32x4 lo, u32x4 hi) {
+    __device__ __forceinline__ void set(const Raw& r) {
         typedef __bf16 pair __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            const unsigned u = w < 4 ? lo[w & 3] : hi[w & 3];
+            const unsigned u = w < 4 ? r.lo[w & 3] : r.hi[w & 3];
             const pair p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.f, false);
             const pair q = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.f, true);
             x[w / 2][4 * (w & 1)] = p[0];
@@ -114,38 +119,49 @@ __device__ __forceinline__ void store_row(Eo* row, int n0, int N, bool wide, con
     }
 }
 
-// 16 bytes per lane from base + off straight into LDS: lane l's land at lds + 16 l.
-// As inline assembly because the compiler, which cannot see that the two buffers of
-// a tile take turns, would wait for the copy before the next LDS read; the wait is
-// step_barrier's.  (No register is loaded; m0 needs the one wait state before it is
-// used.)
-__device__ __forceinline__ void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
+// 16 (4) bytes per lane from base + off straight into LDS: lane l's land at lds +
+// 16 l (4 l).  As inline assembly because the compiler, which cannot see that the
+// buffers of a tile take turns, would wait for the copy before the next LDS read; the
+// waits are step_wait's.  (No register is loaded; m0 needs the one wait state before
+// it is used.)
+__device__ __forceinline__ void copy16_to_lds(const void* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :
                  : "v"(off), "s"(base), "s"(lds)
                  : "memory");
 }
-// every copy and LDS access of this wave is done, and every wave is here
-__device__ __forceinline__ void step_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+__device__ __forceinline__ void copy4_to_lds(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "memory");
+}
+// this wave's LDS accesses are done, and its copies but the last N; every wave is here
+template <int N> __device__ __forceinline__ void step_wait() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
-// Tiles of BM x BN, WM x WN waves, one block of k per step.  Both operands of a
-// step are copied straight into LDS (16 bytes per lane, 8 rows of 128 bytes per
-// wave and instruction) one step ahead of their use; a row's eight 16-byte pieces
-// are stored in an order that depends on the row (the lane that writes a place
-// chooses what it loads), so that the 16 rows a fragment reads at one k lie in
-// different banks.  Rows behind the last one of A or B are copies of it, whose
-// products are not stored.  A last, partial block goes through registers, with
-// zeros behind K.
-template <int BM, int BN, int WM, int WN, typename Eo>
+// Tiles of BM x BN, WM x WN waves, one block of k per step, S steps of operands in
+// LDS.  Both operands and A's scales are copied straight there (8 rows of 128 bytes
+// per wave and instruction); a row's eight 16-byte pieces are stored in an order that
+// depends on the row (the lane that writes a place chooses what it loads), so that the
+// 16 rows a fragment reads at one k lie in different banks.  Rows behind the last one
+// of A or B are copies of it, whose products are not stored; pieces behind K are
+// zeros.
+// The one barrier of a step stands before the products of its last row of fragments:
+// by then everybody has read the step's operands, whose buffer is filled anew, and
+// has its part of the next step's, whose first fragments are read while those
+// products run.
+template <int BM, int BN, int WM, int WN, int S, typename Eo>
 __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int PIECES = (BM + BN) / 8, PW = PIECES / W, PA = BM / 8 / W;
-    static_assert(BM / 8 % W == 0 && BN / 8 % W == 0 && BM <= 64 * W && BN / WN <= kKB, "tile");
-    __shared__ __attribute__((aligned(16))) uint8_t tile[2][(BM + BN) * kKB];
-    __shared__ float scale[2][64 * W];  // (the first BM of each)
-    const int tid = threadIdx.x, lane = tid & 63, wave = kdn::wave_id();
+    constexpr int SK = 8;  // steps of scales per copy: a cache line is asked for once for eight
+    constexpr int SW = BM / 8 / W;  // such copies of 8 rows per wave
+    static_assert(S - 1 < SK && BM / 8 % W == 0 && BN / 8 % W == 0 && BN / WN <= kKB && TM % 2 == 0, "tile");
+    __shared__ __attribute__((aligned(16))) uint8_t tile[S][(BM + BN) * kKB];
+    __shared__ float scale[2][BM][SK], scale_b[2][W][64];  // (of scale_b's 64, SK count)
+    const int lane = threadIdx.x & 63, wave = kdn::wave_id();
     const int wm = wave % WM, wn = wave / WM;
     // each XCD (workgroups are handed to the eight in turn) takes a run of tiles, and
     // walks it in strips of 8 tiles of m, so that what it reads stays in its L2
@@ -159,43 +175,57 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     const int width = p.mt - 8 * strip < 8 ? p.mt - 8 * strip : 8;
     const int m0 = (8 * strip + in_strip % width) * BM, n0 = (in_strip / width) * BN;
 
+    // where a row's piece c is stored: at c ^ key.  The 64 banks of LDS hold two rows of
+    // 128 bytes, so 16 rows at one k use each bank once if the rows of either parity
+    // have eight different keys.
+    auto key_a = [](int r) { return (r >> 1) & 7; };
+    auto key_b = [](int r) { return ((r / (4 * TN)) & 3) * 2 + ((r >> 1) & 1); };
     // piece = wave + W i: rows 8 piece .. + 7 of A's tile (i < PA), then of B's
     const int row8 = lane >> 3, place = lane & 7;
+    auto piece_row = [&](int i) { return 8 * (wave + W * (i < PA ? i : i - PA)) + row8; };
+    auto piece_k = [&](int i) {
+        const int r = piece_row(i);
+        return 16 * (place ^ (i < PA ? key_a(r) : key_b(r)));
+    };
     uint32_t off[PW];
-    int koff[2];
 #pragma unroll
     for (int i = 0; i < PW; ++i) {
-        const bool is_a = i < PA;
-        const int r = 8 * (wave + W * (is_a ? i : i - PA)) + row8;
-        const int last = (is_a ? p.M - m0 : p.N - n0) - 1;
-        const int key = is_a ? r & 7 : ((r / (4 * TN)) & 1) * 4 + (r & 3);
-        // (the key is the same for all of a wave's pieces: they are 8 W rows apart)
-        koff[is_a ? 0 : 1] = 16 * (place ^ key);
-        off[i] = uint32_t(r < last ? r : last) * uint32_t(p.K) + 16 * (place ^ key);
+        const int r = piece_row(i), last = (i < PA ? p.M - m0 : p.N - n0) - 1;
+        off[i] = uint32_t(r < last ? r : last) * uint32_t(p.K) + uint32_t(piece_k(i));
     }
     const uint8_t* a0 = p.A + size_t(m0) * p.K;
     const uint8_t* b0 = p.B + size_t(n0) * p.K;
-    const uint32_t lds0 = uint32_t(uintptr_t(
-        (__attribute__((address_space(3))) uint8_t*)&tile[0][0]));
-    auto load = [&](int kb, int buf) {
-#pragma unroll
-        for (int i = 0; i < PW; ++i)
-            copy_to_lds((i < PA ? a0 : b0) + size_t(kb) * kKB, off[i],
-                        lds0 + buf * (BM + BN) * kKB + 8 * (wave + W * i) * kKB);
-    };
-    auto load_tail = [&](int kb, int buf) {
-#pragma unroll
-        for (int i = 0; i < PW; ++i) {
-            u32x4 x = {0, 0, 0, 0};
-            if (kb * kKB + koff[i < PA ? 0 : 1] < p.K)
-                x = *reinterpret_cast<const u32x4*>((i < PA ? a0 : b0) + size_t(kb) * kKB + off[i]);
-            *reinterpret_cast<u32x4*>(&tile[buf][8 * (wave + W * i) * kKB + 16 * lane]) = x;
-        }
-    };
-    const int srow = m0 + tid < p.M ? m0 + tid : p.M - 1;
-    const float* sa = p.sA + size_t(srow) * p.kb;
+    const float* s0 = p.sA + size_t(m0) * p.kb;
     const int nb = (n0 + wn * 16 * TN) / kKB, nbs = (p.N + kKB - 1) / kKB;
     const float* sb = p.sB + size_t(nb < nbs ? nb : nbs - 1) * p.kb;
+    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)&tile[0][0]));
+    const uint32_t ldss = uint32_t(uintptr_t((__attribute__((address_space(3))) float*)&scale[0][0][0]));
+    const uint32_t ldsb = uint32_t(uintptr_t((__attribute__((address_space(3))) float*)&scale_b[0][wave][0]));
+    const int full = p.K / kKB;  // whole blocks; p.kb is one more with a partial one
+    auto piece_at = [&](int kb, int i) {  // byte of LDS
+        return kb % S * (BM + BN) * kKB + 8 * (wave + W * i) * kKB;
+    };
+    auto load_piece = [&](int kb, int i) {  // of a whole block
+        copy16_to_lds((i < PA ? a0 : b0) + size_t(kb) * kKB, off[i], lds0 + uint32_t(piece_at(kb, i)));
+    };
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            if (kb < full || kb * kKB + piece_k(i) < p.K) load_piece(kb, i);
+            else *reinterpret_cast<u32x4*>(&tile[0][0] + piece_at(kb, i) + 16 * lane) = u32x4{0, 0, 0, 0};
+        }
+    };
+    // the scales of steps k .. k + SK - 1 (k a multiple of SK; behind K: the last one's)
+    auto load_scales = [&](int k) {
+        const int buf = k / SK & 1, at = lane % SK, col = k + at < p.kb ? at : p.kb - 1 - k;
+#pragma unroll
+        for (int i = 0; i < SW; ++i) {
+            const int r = 8 * (wave + W * i), row = r + lane / SK, last = p.M - m0 - 1;
+            const int from = (row < last ? row : last) * p.kb + col;
+            copy4_to_lds(s0 + k, uint32_t(from) * 4u, ldss + (buf * BM + r) * SK * 4);
+        }
+        copy4_to_lds(sb + k, uint32_t(col) * 4u, ldsb + buf * W * 64 * 4);
+    };
 
     floatx4 acc[TM][TN];
 #pragma unroll
@@ -204,71 +234,99 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
         for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
 
     const int r16 = lane & 15, g = lane >> 4;
-    const int ra = wm * 16 * TM + r16, ka = ra & 7;
+    const int ra = wm * 16 * TM + r16, ka = key_a(ra);
     const int rb = wn * 16 * TN + (r16 / 4) * 4 * TN + (r16 & 3);
-    // the products of one step.  The order is the source's (sched_barrier): the next
-    // row of A is read while this one is multiplied, and a product's multiply-adds
-    // follow DELAY products later, when it is there.
-    auto step = [&](int buf, float sbk) {
-        constexpr int DELAY = TN > 2 ? 2 : 1;
-        const uint8_t* ta = tile[buf] + ra * kKB;
-        const uint8_t* tb = tile[buf] + (BM + rb) * kKB;
-        Block<Eo> fb[TN], fa[2];
-        float s[2];
-        auto read_a = [&](int i) {
-            const uint8_t* q = ta + 16 * i * kKB;
-            fa[i & 1].set(*reinterpret_cast<const u32x4*>(q + 16 * (g ^ ka)),
-                          *reinterpret_cast<const u32x4*>(q + 16 * ((g + 4) ^ ka)));
-            s[i & 1] = scale[buf][ra + 16 * i];
-        };
-        read_a(0);
+    const int kbkey = key_b(rb);  // (the same for rb + 4 j)
+    const int a_lo = ra * kKB + 16 * (g ^ ka), a_hi = ra * kKB + 16 * ((g + 4) ^ ka);
+    const int b_lo = (BM + rb) * kKB + 16 * (g ^ kbkey), b_hi = (BM + rb) * kKB + 16 * ((g + 4) ^ kbkey);
+    constexpr int DIST = TM % 4 == 0 ? 2 : 1, NA = 2 * DIST;  // rows of A read ahead
+    Raw fa[NA], fb[TN];
+    float s[NA], sbk = 0.f;
+    auto read_a = [&](int k, int i) {
+        const int buf = k % S;
+        fa[i % NA].lo = *reinterpret_cast<const u32x4*>(&tile[buf][a_lo + 16 * i * kKB]);
+        fa[i % NA].hi = *reinterpret_cast<const u32x4*>(&tile[buf][a_hi + 16 * i * kKB]);
+        s[i % NA] = scale[k / SK & 1][ra + 16 * i][k % SK];
+    };
+    auto read_b = [&](int buf, int j) {
+        fb[j].lo = *reinterpret_cast<const u32x4*>(&tile[buf][b_lo + 4 * j * kKB]);
+        fb[j].hi = *reinterpret_cast<const u32x4*>(&tile[buf][b_hi + 4 * j * kKB]);
+    };
+    if (p.kb > 0) {
+        load_scales(0);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int key = ((rb / (4 * TN)) & 1) * 4 + (rb & 3);  // (4 j adds nothing)
-            const uint8_t* q = tb + 4 * j * kKB;
-            fb[j].set(*reinterpret_cast<const u32x4*>(q + 16 * (g ^ key)),
-                      *reinterpret_cast<const u32x4*>(q + 16 * ((g + 4) ^ key)));
-        }
-        s[0] *= sbk;
+        for (int k = 0; k < S; ++k)
+            if (k < p.kb) load(k);
+        if (full > S) step_wait<(S - 1) * PW>();
+        else step_wait<0>();
+#pragma unroll
+        for (int i = 0; i < DIST; ++i) read_a(0, i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) read_b(0, j);
+        sbk = scale_b[0][wave][0];
+    }
+    // One step.  In the steps before the last S there is nothing to ask for: LAST is
+    // false.  The order is the source's (sched_barrier): the copies go out one by one
+    // between the products, and a product's multiply-adds follow DELAY products later,
+    // when it is there.
+    auto step = [&](int kb, auto last) {
+        constexpr bool LAST = decltype(last)::value;
+        constexpr int DELAY = TN > 2 ? 2 : 1;
+        constexpr int X0 = (TM - DIST) * TN;  // the barrier
+        constexpr int PER = (PW + DIST * TN - 1) / (DIST * TN);  // copies per product behind it
+        const int nbuf = (kb + 1) % S;
+        Block<Eo> xb[TN], xa;
         floatx4 part[DELAY + 1];
+        float sc[2], sb_next = 0.f;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) xb[j].set(fb[j]);
 #pragma unroll
         for (int x = 0; x < TM * TN + DELAY; ++x) {
+            const int i = x / TN, j = x % TN;
             if (x < TM * TN) {
-                const int i = x / TN, j = x % TN;
-                part[x % (DELAY + 1)] = Block<Eo>::mul(fb[j], fa[i & 1]);
+                if (x == X0) {
+                    // (what is added up by now is, and does not move behind the branches,
+                    // where its products would take registers)
+#pragma unroll
+                    for (int y = 0; y < x - DELAY; ++y) asm volatile("" : "+v"(acc[y / TN][y % TN]));
+                    // the copies of the steps behind the next one stay under way; the
+                    // last steps wait for all
+                    if constexpr (LAST) step_wait<0>();
+                    else step_wait<(S - 2) * PW>();
+                    if (kb % SK == 0 && kb + SK < p.kb) load_scales(kb + SK);
+                }
+                if (j == 0) {
+                    xa.set(fa[i % NA]);
+                    sc[i & 1] = s[i % NA] * sbk;
+                }
+                part[x % (DELAY + 1)] = Block<Eo>::mul(xb[j], xa);
+                // (in the last step this reads what an earlier one left, unused)
+                if (i == TM - 1) read_b(nbuf, j);
+                if (j == 0) read_a(i + DIST < TM ? kb : kb + 1, (i + DIST) % TM);
+                if (x == TM * TN - 1) sb_next = scale_b[(kb + 1) / SK & 1][wave][(kb + 1) % SK];
+                if constexpr (!LAST) {
+                    if (x >= X0)
+#pragma unroll
+                        for (int c = 0; c < PER; ++c)
+                            if ((x - X0) * PER + c < PW) load_piece(kb + S, (x - X0) * PER + c);
+                } else if (x == X0) {
+                    if (kb + S < p.kb) load(kb + S);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (x >= DELAY) {
-                const int y = x - DELAY, i = y / TN, j = y % TN;
+                const int y = x - DELAY, iy = y / TN, jy = y % TN;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = fmaf(part[y % (DELAY + 1)][e], s[i & 1], acc[i][j][e]);
-                // the row before is done: the next one may take its registers
-                if (j == TN - 1 && i + 1 < TM) s[(i + 1) & 1] *= sbk;
+                    acc[iy][jy][e] = fmaf(part[y % (DELAY + 1)][e], sc[iy & 1], acc[iy][jy][e]);
             }
-            if (x % TN == DELAY && x / TN + 1 < TM) read_a(x / TN + 1);
             __builtin_amdgcn_sched_barrier(0);
         }
-    };
-    const int full = p.K / kKB;  // whole blocks; one more if p.kb is larger
-    if (full > 0) load(0, 0);
-    float first = 0.f;
-    if (p.kb > 0) first = sa[0];
-    scale[0][tid] = first;
-    float sbk = p.kb > 0 ? sb[0] : 0.f;
-    for (int kb = 0; kb < full; ++kb) {
-        const int buf = kb & 1, after = kb + 1 < p.kb ? kb + 1 : kb;
-        step_barrier();  // this step's copies have landed, the other buffer is free
-        const float next = sa[after], sb_next = sb[after];
-        if (kb + 1 < full) load(kb + 1, buf ^ 1);
-        step(buf, sbk);
-        scale[buf ^ 1][tid] = next;
         sbk = sb_next;
-    }
-    if (full < p.kb) {
-        load_tail(full, full & 1);  // (its buffer is free since the last barrier)
-        step_barrier();
-        step(full & 1, sbk);
-    }
+    };
+    int kb = 0;
+    for (; kb + S < full; ++kb) step(kb, std::false_type{});
+    for (; kb < p.kb; ++kb) step(kb, std::true_type{});
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = m0 + wm * 16 * TM + 16 * i + r16;
@@ -312,13 +370,13 @@ __global__ __launch_bounds__(64 * W) void qgemm_few_kernel(GemmArgs p) {
         const int k0 = kb * kKB + 16 * g, k1 = k0 + 64;
         const bool in0 = k0 < p.K, in1 = k1 < p.K;
         Block<Eo> fb, fa;
-        fb.set(*(in0 ? reinterpret_cast<const u32x4*>(b + k0) : zeros),
-               *(in1 ? reinterpret_cast<const u32x4*>(b + k1) : zeros));
+        fb.set(Raw{*(in0 ? reinterpret_cast<const u32x4*>(b + k0) : zeros),
+               *(in1 ? reinterpret_cast<const u32x4*>(b + k1) : zeros)});
         const float sbk = sb[kb];
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            fa.set(*(in0 ? reinterpret_cast<const u32x4*>(a[i] + k0) : zeros),
-                   *(in1 ? reinterpret_cast<const u32x4*>(a[i] + k1) : zeros));
+            fa.set(Raw{*(in0 ? reinterpret_cast<const u32x4*>(a[i] + k0) : zeros),
+                   *(in1 ? reinterpret_cast<const u32x4*>(a[i] + k1) : zeros)});
             const float s = sa[i][kb] * sbk;
             const floatx4 part = Block<Eo>::mul(fb, fa);
 #pragma unroll
@@ -355,10 +413,10 @@ kdn_status check_gemm(const kdn_gemm_desc* d) {
     return KDN_OK;
 }
 
-template <int BM, int BN, int WM, int WN, typename Eo> void launch_tiles(GemmArgs a, hipStream_t st) {
+template <int BM, int BN, int WM, int WN, int S, typename Eo> void launch_tiles(GemmArgs a, hipStream_t st) {
     a.mt = (a.M + BM - 1) / BM;
     a.nt = (a.N + BN - 1) / BN;
-    qgemm_kernel<BM, BN, WM, WN, Eo><<<unsigned(a.mt) * unsigned(a.nt), 64 * WM * WN, 0, st>>>(a);
+    qgemm_kernel<BM, BN, WM, WN, S, Eo><<<unsigned(a.mt) * unsigned(a.nt), 64 * WM * WN, 0, st>>>(a);
 }
 
 template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
@@ -373,9 +431,9 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         const int64_t big = int64_t((a.M + 255) / 256) * ((a.N + 255) / 256);
         const int64_t mid = int64_t((a.M + 127) / 128) * ((a.N + 127) / 128);
         // (widened operands leave no registers for the largest tile)
-        if (sizeof(Eo) == 2 && big >= 256) launch_tiles<256, 256, 2, 4, bf16_t>(a, st);
-        else if (mid >= 256) launch_tiles<128, 128, 2, 2, Eo>(a, st);
-        else launch_tiles<64, 64, 2, 2, Eo>(a, st);
+        if (sizeof(Eo) == 2 && big >= 256) launch_tiles<256, 256, 2, 4, 2, bf16_t>(a, st);
+        else if (mid >= 256) launch_tiles<128, 128, 2, 2, 2, Eo>(a, st);
+        else launch_tiles<64, 64, 2, 2, 4, Eo>(a, st);
     }
 }
 
