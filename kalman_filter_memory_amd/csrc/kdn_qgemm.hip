@@ -20,8 +20,7 @@
 //
 // B is the instruction's first operand: a lane then holds consecutive columns n of
 // one row m of C.  Which weight row stands in which row of the instruction is free,
-// and is chosen so that the TN tiles of a wave give each lane 4 TN consecutive
-// columns: C leaves in 16-byte stores.  The order of k inside a block is free as
+// and is chosen so that a lane has 16 bytes of C in one piece (column_of).  The order of k inside a block is free as
 // well (both operands only have to agree): lane group g takes bytes 16 g .. + 15 and
 // 64 + 16 g .. + 15 of the 128.
 #include <hip/hip_runtime.h>
@@ -95,28 +94,11 @@ template <> struct Block<float> {
     }
 };
 
-// n values of one row of C from column n0, in vectors where the row allows it
-template <typename Eo, int NC>
-__device__ __forceinline__ void store_row(Eo* row, int n0, int N, bool wide, const float* f) {
-    constexpr int V = 16 / int(sizeof(Eo));
-#pragma unroll
-    for (int v = 0; v < NC; v += V) {
-        if (wide && NC % V == 0 && n0 + v + V <= N) {
-            u32x4 u;
-            if constexpr (sizeof(Eo) == 2) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = kdn::pack_bf16(f[v + 2 * i], f[v + 2 * i + 1]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(f[v + i]);
-            }
-            *reinterpret_cast<u32x4*>(row + n0 + v) = u;
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (v + i < NC && n0 + v + i < N) row[n0 + v + i] = kdn::from_f<Eo>(f[v + i < NC ? v + i : 0]);
-        }
-    }
+// The column, within a wave's 16 TN, that row r of the j-th instruction's B stands for:
+// a lane's four elements of one instruction (float32) or two (bfloat16) are 16 bytes
+// of C, and the lane groups r / 4 = 0..3 follow each other.
+template <typename Eo> __device__ __forceinline__ int column_of(int j, int r) {
+    return sizeof(Eo) == 2 ? 32 * (j / 2) + 8 * (r / 4) + 4 * (j & 1) + (r & 3) : 16 * j + r;
 }
 
 // 16 (4) bytes per lane from base + off straight into LDS: lane l's land at lds +
@@ -179,7 +161,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     // 128 bytes, so 16 rows at one k use each bank once if the rows of either parity
     // have eight different keys.
     auto key_a = [](int r) { return (r >> 1) & 7; };
-    auto key_b = [](int r) { return ((r / (4 * TN)) & 3) * 2 + ((r >> 1) & 1); };
+    auto key_b = [](int r) {
+        return sizeof(Eo) == 2 ? ((r >> 3) & 3) * 2 + ((r >> 1) & 1) : (r >> 1) & 7;
+    };
     // piece = wave + W i: rows 8 piece .. + 7 of A's tile (i < PA), then of B's
     const int row8 = lane >> 3, place = lane & 7;
     auto piece_row = [&](int i) { return 8 * (wave + W * (i < PA ? i : i - PA)) + row8; };
@@ -235,8 +219,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
 
     const int r16 = lane & 15, g = lane >> 4;
     const int ra = wm * 16 * TM + r16, ka = key_a(ra);
-    const int rb = wn * 16 * TN + (r16 / 4) * 4 * TN + (r16 & 3);
-    const int kbkey = key_b(rb);  // (the same for rb + 4 j)
+    const int rb = wn * 16 * TN + column_of<Eo>(0, r16);
+    const int kbkey = key_b(rb);  // (the same for all j)
     const int a_lo = ra * kKB + 16 * (g ^ ka), a_hi = ra * kKB + 16 * ((g + 4) ^ ka);
     const int b_lo = (BM + rb) * kKB + 16 * (g ^ kbkey), b_hi = (BM + rb) * kKB + 16 * ((g + 4) ^ kbkey);
     constexpr int DIST = TM % 4 == 0 ? 2 : 1, NA = 2 * DIST;  // rows of A read ahead
@@ -249,8 +233,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
         s[i % NA] = scale[k / SK & 1][ra + 16 * i][k % SK];
     };
     auto read_b = [&](int buf, int j) {
-        fb[j].lo = *reinterpret_cast<const u32x4*>(&tile[buf][b_lo + 4 * j * kKB]);
-        fb[j].hi = *reinterpret_cast<const u32x4*>(&tile[buf][b_hi + 4 * j * kKB]);
+        fb[j].lo = *reinterpret_cast<const u32x4*>(&tile[buf][b_lo + column_of<Eo>(j, 0) * kKB]);
+        fb[j].hi = *reinterpret_cast<const u32x4*>(&tile[buf][b_hi + column_of<Eo>(j, 0) * kKB]);
     };
     if (p.kb > 0) {
         load_scales(0);
@@ -327,17 +311,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     int kb = 0;
     for (; kb + S < full; ++kb) step(kb, std::false_type{});
     for (; kb < p.kb; ++kb) step(kb, std::true_type{});
+    // C goes through LDS, rounded, so that a wave writes whole rows of the tile: written
+    // from the fragments, 64 bytes of 16 rows at a time, rows that do not start on a
+    // cache line cost twice the write requests (32768 x 6144 x 2048 into rows of 6192:
+    // 453 against 397 us for rows of 6208).  Pieces of a row are stored in an order that
+    // depends on the row, as above.
+    constexpr int V = 16 / int(sizeof(Eo)), CR = BN / V;  // columns, and pieces of a row
+    static_assert(BM * CR * 16 <= S * (BM + BN) * kKB && CR >= 8, "C fits the operands' place");
+    auto key_c = [](int r) { return CR >= 16 ? r & 15 : (r >> 1) & 7; };
+    u32x4* out = reinterpret_cast<u32x4*>(&tile[0][0]);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int m = m0 + wm * 16 * TM + 16 * i + r16;
-        if (m < p.M) {
-            float f[4 * TN];
+        const int r = ra + 16 * i;
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+        for (int v = 0; v < 4 * TN / V; ++v) {
+            u32x4 u;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[4 * j + e] = acc[i][j][e];
-            store_row<Eo, 4 * TN>(static_cast<Eo*>(p.C) + size_t(m) * p.ldc,
-                                  n0 + wn * 16 * TN + g * 4 * TN, p.N, p.wide != 0, f);
+            for (int w = 0; w < 4; ++w) {
+                if constexpr (sizeof(Eo) == 2) {
+                    const floatx4& t = acc[i][2 * v + w / 2];
+                    u[w] = kdn::pack_bf16(t[2 * (w & 1)], t[2 * (w & 1) + 1]);
+                } else {
+                    u[w] = __float_as_uint(acc[i][v][w]);
+                }
+            }
+            out[r * CR + ((wn * 16 * TN / V + 4 * v + g) ^ key_c(r))] = u;
+        }
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int o = threadIdx.x; o < BM * CR; o += 64 * W) {
+        const int r = o / CR, c = o % CR, m = m0 + r, n = n0 + c * V;
+        const u32x4 u = out[r * CR + (c ^ key_c(r))];
+        if (m < p.M && n < p.N) {
+            Eo* row = static_cast<Eo*>(p.C) + size_t(m) * p.ldc;
+            if (p.wide && n + V <= p.N) {
+                *reinterpret_cast<u32x4*>(row + n) = u;
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (n + e < p.N) {
+                        if constexpr (sizeof(Eo) == 2) row[n + e] = bf16_t(u[e / 2] >> (16 * (e & 1)));
+                        else row[n + e] = __uint_as_float(u[e]);
+                    }
+            }
         }
     }
 }
