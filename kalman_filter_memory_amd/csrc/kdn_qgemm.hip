@@ -360,7 +360,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     }
 }
 
-// Few rows of A (up to 16 TM): the weights are what has to be read, once, and every
+// Few rows of A (up to 16 TM, TM 1 or 2): the weights are what has to be read, once, and every
 // workgroup has to have its share of them in flight at once.  A workgroup takes 16
 // columns and all of K, its W waves the blocks w, w + W, ...; fragments go from
 // memory straight into registers, and the waves' sums meet in LDS in their order.
@@ -439,19 +439,30 @@ template <int BM, int BN, int WM, int WN, int S, typename Eo> void launch_tiles(
 
 template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
     const unsigned cols = unsigned((a.N + 15) / 16);
+    // Up to 32 rows: 32 x 2048 x 8192 takes 16.3 us against 21.0 in tiles of 64 x 64, 16 x
+    // 8192 x 8192 19.8 against 34.0; at 48 x 6192 x 2048 the tiles are ahead, 7.4 against
+    // 12.5 with three times 16 rows.
     if (a.M <= 16) {
         qgemm_few_kernel<1, 8, Eo><<<cols, 512, 0, st>>>(a);
     } else if (a.M <= 32) {
         qgemm_few_kernel<2, 8, Eo><<<cols, 512, 0, st>>>(a);
-    } else if (a.M <= 64) {
-        qgemm_few_kernel<4, 8, Eo><<<cols, 512, 0, st>>>(a);
     } else {
+        // The larger the tile, the less is read per product, as long as the tiles fill
+        // the 256 CUs.  Tiles of 128 x 128 run two to a CU and end one by one; a round of
+        // 256 tiles of 256 x 256, one to a CU, takes as long as 712 of them (us, bfloat16,
+        // K 2048): 4096 x 6192 (400 large tiles, two rounds) 57.5 in large ones against
+        // 63.1, 3000 x 6192 (300, two rounds) 66.0 against 53.4.  Against 64 x 64: 512 x
+        // 6192 is 196 tiles of 128 x 128 and takes 13.4 in them against 15.7, 1024 x 2048
+        // is 128 and takes 11.8 against 9.9.  (Widened operands leave no registers for
+        // the largest tile.)
         const int64_t big = int64_t((a.M + 255) / 256) * ((a.N + 255) / 256);
         const int64_t mid = int64_t((a.M + 127) / 128) * ((a.N + 127) / 128);
-        // (widened operands leave no registers for the largest tile)
-        if (sizeof(Eo) == 2 && big >= 256) launch_tiles<256, 256, 2, 4, 2, bf16_t>(a, st);
-        else if (mid >= 256) launch_tiles<128, 128, 2, 2, 2, Eo>(a, st);
-        else launch_tiles<64, 64, 2, 2, 4, Eo>(a, st);
+        if (sizeof(Eo) == 2 && (big + 255) / 256 * 712 <= mid)
+            launch_tiles<256, 256, 2, 4, 2, bf16_t>(a, st);
+        else if (mid >= 192)
+            launch_tiles<128, 128, 2, 2, 2, Eo>(a, st);
+        else
+            launch_tiles<64, 64, 2, 2, 2, Eo>(a, st);
     }
 }
 
