@@ -475,7 +475,7 @@ kdn_status kdn_quantize(const kdn_quant_desc *n, const void *x, void *q, float *
  * (block_rows 128), C [M, N] in dtype with rows ldc >= N elements apart (what
  * lies behind the N columns of a row is not written).  Sums are float32, rounded
  * once into C.  K a multiple of 16 (0: C is zero) up to 2^23, the other sizes up to
- * 2^28, and fewer than 2^22 tiles of 64 x 64 of C (KDN_ERR_UNSUPPORTED otherwise).  A, B and C
+ * 2^26, and fewer than 2^22 tiles of 64 x 64 of C (KDN_ERR_UNSUPPORTED otherwise).  A, B and C
  * 16-byte aligned; C must not alias an input. */
 typedef struct {
     int32_t M, N, K, ldc;

@@ -703,6 +703,13 @@ def _shaped(name, x, dtype, shape):
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
 
 
+def _int32(*sizes):
+    """The sizes, for a descriptor's 32-bit fields (which would cut larger ones)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"a size is beyond 32 bits: {sizes}")
+    return list(sizes)
+
+
 def _launch(name, dev, *args):
     """A library call with `dev` current and its current torch stream as the last
     argument.  (The stream's handle as torch keeps it: building a Stream object for it
@@ -733,7 +740,7 @@ def _norm_desc(x, name, weight, residual_dtype, eps):
         raise ValueError(f"{name} must have a last dimension")
     d = x.shape[-1]
     _shaped("weight", weight, torch.float32, (d,))
-    return KdnNormDesc(x.numel() // d if d else 0, d, _dtype_code(x.dtype),
+    return KdnNormDesc(x.numel() // d if d else 0, *_int32(d), _dtype_code(x.dtype),
                        _dtype_code(residual_dtype), eps)
 
 
@@ -804,7 +811,7 @@ def quantize(x, block_rows=1):
     if x.dim() == 0 or (block_rows != 1 and x.dim() != 2):
         raise ValueError("x must be [..., d], and [rows, d] for blocks of several rows")
     *lead, d = x.shape
-    n = KdnQuantDesc(x.numel() // d if d else 0, d, block_rows, _dtype_code(x.dtype))
+    n = KdnQuantDesc(x.numel() // d if d else 0, *_int32(d, block_rows), _dtype_code(x.dtype))
     if block_rows != 1:
         lead = [-(-lead[0] // max(1, block_rows))]
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
@@ -829,7 +836,7 @@ def quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     kb = -(-K // 128)
     _shaped("a_scale", a_scale, torch.float32, (*lead, kb))
     _shaped("b_scale", b_scale, torch.float32, (-(-N // 128), kb))
-    d = KdnGemmDesc(lead.numel(), N, K, N, _dtype_code(out_dtype))
+    d = KdnGemmDesc(*_int32(lead.numel(), N, K, N), _dtype_code(out_dtype))
     c = _empty((*lead, N), out_dtype, dev)
     _launch("kdn_quant_gemm", dev, ctypes.byref(d), _ptr(a), _ptr(a_scale), _ptr(b),
             _ptr(b_scale), _ptr(c))
@@ -864,7 +871,7 @@ def layer_quant_forward(x, norm_weight, W_in, W_in_scale, b_gate, W_out, W_out_s
     _shaped("b_gate", b_gate, f32, (3 * H,))
     _shaped("W_out", W_out, fp8, (D, n_out))
     _shaped("W_out_scale", W_out_scale, f32, (-(-D // 128), -(-n_out // 128)))
-    d = make_layer_desc(B, T, H, D, d_k, d_v, chunk, variant, _dtype_code(x.dtype))
+    d = make_layer_desc(*_int32(B, T, H, D), d_k, d_v, chunk, variant, _dtype_code(x.dtype))
     lam_shape = (B, H, d_k) if d.variant == DIAGONAL else (B, H)
     _shaped("lambda0", lambda0, f32, lam_shape)
     _shaped("S0", S0, f32, (B, H, d_v, d_k))
@@ -885,7 +892,7 @@ def layer_quant_forward(x, norm_weight, W_in, W_in_scale, b_gate, W_out, W_out_s
 
 
 def make_scan_desc(B, H, T, d, dtype, gate_dtype) -> KdnScanDesc:
-    return KdnScanDesc(B, H, T, d, dtype, gate_dtype)
+    return KdnScanDesc(*_int32(B, H, T, d), dtype, gate_dtype)
 
 
 def gated_scan(x, a, h0=None):

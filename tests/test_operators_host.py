@@ -161,6 +161,21 @@ def test_scan_refuses_arguments(lib):
     assert step(ctypes.byref(_scan(B=0)), *([None] * 4), 1, None, None) == 0
 
 
+def test_binding_refuses_sizes_beyond_the_descriptors(lib):
+    """Sizes that a 32-bit field would cut are refused, not cut (tensors without
+    storage stand in for ones of that size)."""
+    import torch
+    big = (1 << 32) + 64
+    with pytest.raises(ValueError):
+        kdn._int32(big)
+    with pytest.raises(ValueError):
+        kdn.make_scan_desc(1, 1, big, 64, kdn.F32, kdn.F32)
+    with pytest.raises(ValueError):
+        kdn._norm_desc(torch.empty(1, big, device="meta"), "x", torch.empty(big, device="meta"),
+                       torch.float32, 1e-6)
+    assert kdn._int32(5, (1 << 31) - 1) == [5, (1 << 31) - 1]
+
+
 def test_binding_refuses_cpu_tensors(lib):
     import torch
     x = torch.zeros(2, 64)
@@ -176,7 +191,7 @@ def test_binding_refuses_cpu_tensors(lib):
 
 GEMM_BAD = [
     (dict(M=-1), 2), (dict(N=-1), 2), (dict(K=-16), 2), (dict(ldc=199), 2), (dict(K=24), 3),
-    (dict(dtype=2), 3), (dict(K=(1 << 23) + 16), 3), (dict(M=(1 << 28) + 1), 3),
+    (dict(dtype=2), 3), (dict(K=(1 << 23) + 16), 3), (dict(M=(1 << 26) + 1), 3), (dict(N=(1 << 26) + 1, ldc=(1 << 26) + 1), 3), (dict(ldc=(1 << 26) + 1), 3),
     (dict(M=1 << 20, N=1 << 20, ldc=1 << 20), 3),
 ]
 
