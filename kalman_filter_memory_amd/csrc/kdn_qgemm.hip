@@ -134,16 +134,24 @@ template <int N> __device__ __forceinline__ void step_wait() {
 // by then everybody has read the step's operands, whose buffer is filled anew, and
 // has its part of the next step's, whose first fragments are read while those
 // products run.
-template <int BM, int BN, int WM, int WN, int S, typename Eo>
-__global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
+//
+// KS groups of such waves share the steps (group i takes blocks i, i + KS, ...), each
+// with its own buffers, and their sums meet at the end, the first group's first: a
+// small tile leaves a SIMD one wave, whose instructions (in float32 the conversions),
+// not the matrix unit, set the pace.
+template <int BM, int BN, int WM, int WN, int S, int KS, typename Eo>
+__global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p) {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int PIECES = (BM + BN) / 8, PW = PIECES / W, PA = BM / 8 / W;
     constexpr int SK = 8;  // steps of scales per copy: a cache line is asked for once for eight
     constexpr int SW = BM / 8 / W;  // such copies of 8 rows per wave
     static_assert(S - 1 < SK && BM / 8 % W == 0 && BN / 8 % W == 0 && BN / WN <= kKB && TM % 2 == 0, "tile");
-    __shared__ __attribute__((aligned(16))) uint8_t tile[S][(BM + BN) * kKB];
-    __shared__ float scale[2][BM][SK], scale_b[2][W][64];  // (of scale_b's 64, SK count)
-    const int lane = threadIdx.x & 63, wave = kdn::wave_id();
+    __shared__ __attribute__((aligned(16))) uint8_t tiles[KS][S][(BM + BN) * kKB];
+    __shared__ float scales[KS][2][BM][SK], scales_b[KS][2][W][64];  // (of 64, SK count)
+    const int lane = threadIdx.x & 63, wave = kdn::wave_id() % W, grp = kdn::wave_id() / W;
+    auto& tile = tiles[grp];
+    auto& scale = scales[grp];
+    auto& scale_b = scales_b[grp];
     const int wm = wave % WM, wn = wave / WM;
     // each XCD (workgroups are handed to the eight in turn) takes a run of tiles, and
     // walks it in strips of 6 tiles of m, so that its 32 CUs work on about 6 x 5 tiles at
@@ -189,29 +197,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     const uint32_t ldss = uint32_t(uintptr_t((__attribute__((address_space(3))) float*)&scale[0][0][0]));
     const uint32_t ldsb = uint32_t(uintptr_t((__attribute__((address_space(3))) float*)&scale_b[0][wave][0]));
     const int full = p.K / kKB;  // whole blocks; p.kb is one more with a partial one
-    auto piece_at = [&](int kb, int i) {  // byte of LDS
-        return kb % S * (BM + BN) * kKB + 8 * (wave + W * i) * kKB;
+    const int steps = (p.kb + KS - 1) / KS;
+    auto block_of = [&](int step) { return step * KS + grp; };
+    auto piece_at = [&](int k, int i) {  // byte of LDS
+        return k % S * (BM + BN) * kKB + 8 * (wave + W * i) * kKB;
     };
-    auto load_piece = [&](int kb, int i) {  // of a whole block
-        copy16_to_lds((i < PA ? a0 : b0) + size_t(kb) * kKB, off[i], lds0 + uint32_t(piece_at(kb, i)));
+    auto load_piece = [&](int k, int i) {  // of a whole block
+        copy16_to_lds((i < PA ? a0 : b0) + size_t(block_of(k)) * kKB, off[i],
+                      lds0 + uint32_t(piece_at(k, i)));
     };
-    auto load = [&](int kb) {
+    auto load = [&](int k) {
+        const int kb = block_of(k);
 #pragma unroll
         for (int i = 0; i < PW; ++i) {
-            if (kb < full || kb * kKB + piece_k(i) < p.K) load_piece(kb, i);
-            else *reinterpret_cast<u32x4*>(&tile[0][0] + piece_at(kb, i) + 16 * lane) = u32x4{0, 0, 0, 0};
+            if (kb < full || kb * kKB + piece_k(i) < p.K) load_piece(k, i);
+            else *reinterpret_cast<u32x4*>(&tile[0][0] + piece_at(k, i) + 16 * lane) = u32x4{0, 0, 0, 0};
         }
     };
     // the scales of steps k .. k + SK - 1 (k a multiple of SK; behind K: the last one's)
     auto load_scales = [&](int k) {
-        const int buf = k / SK & 1, at = lane % SK, col = k + at < p.kb ? at : p.kb - 1 - k;
+        const int buf = k / SK & 1, kb = block_of(k + lane % SK), col = kb < p.kb ? kb : p.kb - 1;
 #pragma unroll
         for (int i = 0; i < SW; ++i) {
             const int r = 8 * (wave + W * i), row = r + lane / SK, last = p.M - m0 - 1;
             const int from = (row < last ? row : last) * p.kb + col;
-            copy4_to_lds(s0 + k, uint32_t(from) * 4u, ldss + (buf * BM + r) * SK * 4);
+            copy4_to_lds(s0, uint32_t(from) * 4u, ldss + (buf * BM + r) * SK * 4);
         }
-        copy4_to_lds(sb + k, uint32_t(col) * 4u, ldsb + buf * W * 64 * 4);
+        copy4_to_lds(sb, uint32_t(col) * 4u, ldsb + buf * W * 64 * 4);
     };
 
     floatx4 acc[TM][TN];
@@ -243,8 +255,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
         load_scales(0);
 #pragma unroll
         for (int k = 0; k < S; ++k)
-            if (k < p.kb) load(k);
-        if (full > S) step_wait<(S - 1) * PW>();
+            if (k < steps) load(k);
+        if (full >= (S + 1) * KS) step_wait<(S - 1) * PW>();
         else step_wait<0>();
 #pragma unroll
         for (int i = 0; i < DIST; ++i) read_a(0, i);
@@ -256,12 +268,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
     // false.  The order is the source's (sched_barrier): the copies go out one by one
     // between the products, and a product's multiply-adds follow DELAY products later,
     // when it is there.
-    auto step = [&](int kb, auto last) {
+    auto step = [&](int k, auto last) {
         constexpr bool LAST = decltype(last)::value;
         constexpr int DELAY = TN > 2 ? 2 : 1;
         constexpr int X0 = (TM - DIST) * TN;  // the barrier
         constexpr int PER = (PW + DIST * TN - 1) / (DIST * TN);  // copies per product behind it
-        const int nbuf = (kb + 1) % S;
+        const int nbuf = (k + 1) % S;
+        const bool live = KS == 1 || block_of(k) < p.kb;  // (else zeros, whatever their scale)
         Block<Eo> xb[TN], xa;
         floatx4 part[DELAY + 1];
         float sc[2], sb_next = 0.f;
@@ -280,24 +293,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
                     // last steps wait for all
                     if constexpr (LAST) step_wait<0>();
                     else step_wait<(S - 2) * PW>();
-                    if (kb % SK == 0 && kb + SK < p.kb) load_scales(kb + SK);
+                    if (k % SK == 0 && k + SK < steps) load_scales(k + SK);
                 }
                 if (j == 0) {
                     xa.set(fa[i % NA]);
-                    sc[i & 1] = s[i % NA] * sbk;
+                    sc[i & 1] = live ? s[i % NA] * sbk : 0.f;
                 }
                 part[x % (DELAY + 1)] = Block<Eo>::mul(xb[j], xa);
                 // (in the last step this reads what an earlier one left, unused)
                 if (i == TM - 1) read_b(nbuf, j);
-                if (j == 0) read_a(i + DIST < TM ? kb : kb + 1, (i + DIST) % TM);
-                if (x == TM * TN - 1) sb_next = scale_b[(kb + 1) / SK & 1][wave][(kb + 1) % SK];
+                if (j == 0) read_a(i + DIST < TM ? k : k + 1, (i + DIST) % TM);
+                if (x == TM * TN - 1) sb_next = scale_b[(k + 1) / SK & 1][wave][(k + 1) % SK];
                 if constexpr (!LAST) {
                     if (x >= X0)
 #pragma unroll
                         for (int c = 0; c < PER; ++c)
-                            if ((x - X0) * PER + c < PW) load_piece(kb + S, (x - X0) * PER + c);
+                            if ((x - X0) * PER + c < PW) load_piece(k + S, (x - X0) * PER + c);
                 } else if (x == X0) {
-                    if (kb + S < p.kb) load(kb + S);
+                    if (k + S < steps) load(k + S);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -311,18 +324,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
         }
         sbk = sb_next;
     };
-    int kb = 0;
-    for (; kb + S < full; ++kb) step(kb, std::false_type{});
-    for (; kb < p.kb; ++kb) step(kb, std::true_type{});
+    int k = 0;
+    for (; (k + S + 1) * KS <= full; ++k) step(k, std::false_type{});
+    for (; k < steps; ++k) step(k, std::true_type{});
+    if constexpr (KS > 1) {
+        static_assert(KS == 2 && BM * BN * 4 <= int(sizeof(tiles)), "two groups");
+        floatx4* sums = reinterpret_cast<floatx4*>(&tiles[0][0][0]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i)
+            if (grp == 1) sums[(i * W + wave) * 64 + lane] = acc[i / TN][i % TN];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i)
+            if (grp == 0) acc[i / TN][i % TN] += sums[(i * W + wave) * 64 + lane];
+    }
     // C goes through LDS, rounded, so that a wave writes whole rows of the tile: written
     // from the fragments, 64 bytes of 16 rows at a time, rows that do not start on a
     // cache line cost twice the write requests (32768 x 6144 x 2048 into rows of 6192:
     // 453 against 397 us for rows of 6208).  Pieces of a row are stored in an order that
     // depends on the row, as above.
     constexpr int V = 16 / int(sizeof(Eo)), CR = BN / V;  // columns, and pieces of a row
-    static_assert(BM * CR * 16 <= S * (BM + BN) * kKB && CR >= 8, "C fits the operands' place");
+    static_assert(BM * CR * 16 <= int(sizeof(tiles)) && CR >= 8, "C fits the operands' place");
     auto key_c = [](int r) { return CR >= 16 ? r & 15 : (r >> 1) & 7; };
-    u32x4* out = reinterpret_cast<u32x4*>(&tile[0][0]);
+    u32x4* out = reinterpret_cast<u32x4*>(&tiles[0][0][0]);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -339,12 +364,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void qgemm_kernel(GemmArgs p) {
                     u[w] = __float_as_uint(acc[i][v][w]);
                 }
             }
-            out[r * CR + ((wn * 16 * TN / V + 4 * v + g) ^ key_c(r))] = u;
+            if (grp == 0) out[r * CR + ((wn * 16 * TN / V + 4 * v + g) ^ key_c(r))] = u;
         }
     }
     __syncthreads();
 #pragma unroll 4
-    for (int o = threadIdx.x; o < BM * CR; o += 64 * W) {
+    for (int o = threadIdx.x; o < BM * CR; o += 64 * W * KS) {
         const int r = o / CR, c = o % CR, m = m0 + r, n = n0 + c * V;
         const u32x4 u = out[r * CR + (c ^ key_c(r))];
         if (m < p.M && n < p.N) {
@@ -435,10 +460,11 @@ kdn_status check_gemm(const kdn_gemm_desc* d) {
     return KDN_OK;
 }
 
-template <int BM, int BN, int WM, int WN, int S, typename Eo> void launch_tiles(GemmArgs a, hipStream_t st) {
+template <int BM, int BN, int WM, int WN, int S, int KS, typename Eo> void launch_tiles(GemmArgs a, hipStream_t st) {
     a.mt = (a.M + BM - 1) / BM;
     a.nt = (a.N + BN - 1) / BN;
-    qgemm_kernel<BM, BN, WM, WN, S, Eo><<<unsigned(a.mt) * unsigned(a.nt), 64 * WM * WN, 0, st>>>(a);
+    qgemm_kernel<BM, BN, WM, WN, S, KS, Eo>
+        <<<unsigned(a.mt) * unsigned(a.nt), 64 * WM * WN * KS, 0, st>>>(a);
 }
 
 template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
@@ -458,15 +484,21 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         // 63.1, 3000 x 6192 (300, two rounds) 66.0 against 53.4.  Against 64 x 64: 512 x
         // 6192 is 196 tiles of 128 x 128 and takes 13.4 in them against 15.7, 1024 x 2048
         // is 128 and takes 11.8 against 9.9.  (Widened operands leave no registers for
-        // the largest tile.)
+        // the largest tile.)  Two groups of waves per 64 x 64 tile while all tiles run at
+        // once, two to a CU, and K is long enough: 256 x 2048 x 2048 7.3 -> 6.8 (float32
+        // 10.4 -> 9.0), 509 x 2048 x 2064 8.8 -> 8.6 (11.8 -> 10.7); but 384 x 6192 x 2048,
+        // 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8.
+        const int64_t few = int64_t((a.M + 63) / 64) * ((a.N + 63) / 64);
         const int64_t big = int64_t((a.M + 255) / 256) * ((a.N + 255) / 256);
         const int64_t mid = int64_t((a.M + 127) / 128) * ((a.N + 127) / 128);
         if (sizeof(Eo) == 2 && (big + 255) / 256 * 712 <= mid)
-            launch_tiles<256, 256, 2, 4, 2, bf16_t>(a, st);
+            launch_tiles<256, 256, 2, 4, 2, 1, bf16_t>(a, st);
         else if (mid >= 192)
-            launch_tiles<128, 128, 2, 2, 2, Eo>(a, st);
+            launch_tiles<128, 128, 2, 2, 2, 1, Eo>(a, st);
+        else if (a.kb >= 8 && few <= 512)
+            launch_tiles<64, 64, 2, 2, 2, 2, Eo>(a, st);
         else
-            launch_tiles<64, 64, 2, 2, 2, Eo>(a, st);
+            launch_tiles<64, 64, 2, 2, 2, 1, Eo>(a, st);
     }
 }
 

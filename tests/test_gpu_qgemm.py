@@ -59,6 +59,7 @@ SHAPES = [
     (1, 1, 16), (1, 16, 128), (1, 200, 2048), (3, 130, 144), (16, 128, 256), (17, 257, 1040),
     (32, 64, 112), (33, 100, 128), (64, 1000, 8192), (65, 65, 16), (65, 300, 272), (100, 129, 4112),
     (128, 128, 128), (129, 1, 384), (257, 513, 640), (509, 2048, 2064), (2000, 2100, 400),
+    (40, 70, 1024), (200, 300, 1040), (300, 190, 1168), (64, 64, 3200), (448, 4000, 2048), (450, 4100, 1040),
     (2048, 2048, 2048), (4095, 4100, 1168), (4096, 4096, 256), (70, 6192, 2048), (5000, 24, 96),
 ]
 
@@ -130,6 +131,25 @@ def test_product_keeps_nan_to_its_row_and_column():
         assert torch.isnan(c[3]).all() and torch.isnan(c[:, 150]).all()
         rows, cols = [i for i in range(M) if i != 3], [i for i in range(200) if i != 150]
         assert torch.equal(c[rows][:, cols], clean[rows][:, cols])
+
+
+def test_product_with_an_infinite_scale():
+    """A row whose scale is infinite is infinite (or NaN where its sum in that block is
+    zero), in tiles as in the kernel for few rows, also where the blocks are shared out
+    and one share has one less; the others stay."""
+    for K in (1040, 1168, 1152, 272):
+        a, sa, b, sb = _operands(100, 200, K, seed=47)
+        a = torch.where(a.float() == 0, 1.0, a.float()).to(a.dtype)
+        b = torch.where(b.float() == 0, 1.0, b.float()).to(b.dtype)
+        clean = kdn.quant_matmul(a, sa, b, sb)
+        sa[7, -1] = float("inf")
+        c = kdn.quant_matmul(a, sa, b, sb)
+        assert not torch.isfinite(c[7]).any()
+        s = kdn.quant_matmul(a[7:8].contiguous(), sa[7:8].contiguous(), b, sb)
+        assert torch.equal(torch.isnan(c[7]), torch.isnan(s[0]))
+        assert torch.equal(c[7][~torch.isnan(c[7])], s[0][~torch.isnan(s[0])])
+        keep = [i for i in range(100) if i != 7]
+        assert torch.equal(c[keep], clean[keep])
 
 
 def test_product_of_no_rows_columns_or_depth():
