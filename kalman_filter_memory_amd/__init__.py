@@ -686,20 +686,21 @@ def decode_step_indexed(q, k, v, a, qnoise, r, S_cache, lam_cache, slot, variant
 def _tensors(*named):
     """Checks (name, tensor) pairs, None among them: on one GPU, contiguous.
     Returns that device."""
-    dev = None
+    dev = at = None
     for name, x in named:
         if x is None:
             continue
-        _gpu(x, name)
+        if not (isinstance(x, torch.Tensor) and x.is_cuda and x.is_contiguous()):
+            _gpu(x, name)
         if dev is None:
-            dev = x.device
-        elif x.device != dev:
+            dev, at = x.device, x.get_device()
+        elif x.get_device() != at:
             raise ValueError(f"{name} is on {x.device}, the other tensors are on {dev}")
     return dev
 
 
 def _shaped(name, x, dtype, shape):
-    if x is not None and (x.dtype != dtype or tuple(x.shape) != tuple(shape)):
+    if x is not None and (x.dtype != dtype or x.shape != shape):
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
 
 
@@ -707,7 +708,7 @@ def _int32(*sizes):
     """The sizes, for a descriptor's 32-bit fields (which would cut larger ones)."""
     if max(sizes) > 0x7FFFFFFF:
         raise ValueError(f"a size is beyond 32 bits: {sizes}")
-    return list(sizes)
+    return sizes
 
 
 def _launch(name, dev, *args):
@@ -729,10 +730,11 @@ def _empty(shape, dtype, dev):
     """torch.empty with dense strides (which empty_strided gives in two thirds of the
     time)."""
     strides, n = [], 1
-    for d in reversed(shape):
+    for d in shape[:0:-1]:
         strides.append(n)
-        n *= max(d, 1)
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=dev)
+        n *= d or 1
+    strides.append(n)
+    return torch.empty_strided(shape, strides[::-1] if shape else (), dtype=dtype, device=dev)
 
 
 def _norm_desc(x, name, weight, residual_dtype, eps):
@@ -764,8 +766,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, in_place=False):
     s = _norm_stream(x, residual, in_place)
     y = torch.empty_like(x)
     rstd = _empty(x.shape[:-1], torch.float32, dev)
-    _launch("kdn_rms_norm", dev, ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(weight), _ptr(y),
-            _ptr(s), _ptr(rstd))
+    _launch("kdn_rms_norm", dev, ctypes.byref(n), x.data_ptr(), _ptr(residual), weight.data_ptr(),
+            y.data_ptr(), _ptr(s), rstd.data_ptr())
     return y, x if s is None else s, rstd
 
 
@@ -777,8 +779,8 @@ def rms_norm_quant(x, weight, residual=None, eps=1e-6, in_place=False):
     s = _norm_stream(x, residual, in_place)
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scale = _empty((*x.shape[:-1], -(-n.d // 128)), torch.float32, dev)
-    _launch("kdn_rms_norm_quant", dev, ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(weight),
-            _ptr(q), _ptr(scale), _ptr(s), None)
+    _launch("kdn_rms_norm_quant", dev, ctypes.byref(n), x.data_ptr(), _ptr(residual),
+            weight.data_ptr(), q.data_ptr(), scale.data_ptr(), _ptr(s), None)
     return q, scale, x if s is None else s
 
 
@@ -816,7 +818,7 @@ def quantize(x, block_rows=1):
         lead = [-(-lead[0] // max(1, block_rows))]
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scale = _empty((*lead, -(-d // 128)), torch.float32, dev)
-    _launch("kdn_quantize", dev, ctypes.byref(n), _ptr(x), _ptr(q), _ptr(scale))
+    _launch("kdn_quantize", dev, ctypes.byref(n), x.data_ptr(), q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -838,8 +840,8 @@ def quant_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     _shaped("b_scale", b_scale, torch.float32, (-(-N // 128), kb))
     d = KdnGemmDesc(*_int32(lead.numel(), N, K, N), _dtype_code(out_dtype))
     c = _empty((*lead, N), out_dtype, dev)
-    _launch("kdn_quant_gemm", dev, ctypes.byref(d), _ptr(a), _ptr(a_scale), _ptr(b),
-            _ptr(b_scale), _ptr(c))
+    _launch("kdn_quant_gemm", dev, ctypes.byref(d), a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
+            b_scale.data_ptr(), c.data_ptr())
     return c
 
 
@@ -954,6 +956,6 @@ def gated_scan_step(x, a, h, slot=None, out=None):
     _shaped("out", out, x.dtype, x.shape)
     s = make_scan_desc(B, H, 1, d, _dtype_code(x.dtype), _dtype_code(a.dtype))
     o = out if out is not None else torch.empty_like(x)
-    _launch("kdn_gated_scan_step", dev, ctypes.byref(s), _ptr(x), _ptr(a), _ptr(h), _ptr(slot),
-            n_slots, _ptr(o))
+    _launch("kdn_gated_scan_step", dev, ctypes.byref(s), x.data_ptr(), a.data_ptr(), h.data_ptr(),
+            _ptr(slot), n_slots, o.data_ptr())
     return o

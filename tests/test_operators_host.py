@@ -173,7 +173,7 @@ def test_binding_refuses_sizes_beyond_the_descriptors(lib):
     with pytest.raises(ValueError):
         kdn._norm_desc(torch.empty(1, big, device="meta"), "x", torch.empty(big, device="meta"),
                        torch.float32, 1e-6)
-    assert kdn._int32(5, (1 << 31) - 1) == [5, (1 << 31) - 1]
+    assert kdn._int32(5, (1 << 31) - 1) == (5, (1 << 31) - 1)
 
 
 def test_binding_refuses_cpu_tensors(lib):
