@@ -192,7 +192,8 @@ __global__ __launch_bounds__(256) void layer_out_kernel(const E* __restrict__ o,
 }
 
 // o [B,H,T,DV] -> token rows [B*T, H*DV] in 8 bits with a scale per 128 columns: 16
-// lanes per block of 128, as in the quantiser, one workgroup per token row
+// lanes per block of 128, as in the quantiser, one workgroup per token row.  B8 T4096
+// H16 d_v 128 bfloat16: 39 us for 203 MB (5.2 TB/s).
 template <typename E, int DV>
 __global__ __launch_bounds__(256) void layer_out_quant_kernel(const E* __restrict__ o,
                                                               uint8_t* __restrict__ q,

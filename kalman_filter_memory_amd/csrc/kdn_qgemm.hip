@@ -134,6 +134,10 @@ template <int N> __device__ __forceinline__ void step_wait() {
 // by then everybody has read the step's operands, whose buffer is filled anew, and
 // has its part of the next step's, whose first fragments are read while those
 // products run.
+// Measured (bfloat16 results): 8192^3 425 us, 2.6 PFLOP/s; 32768 x 6192 x 2048 406 us, 2.05
+// PFLOP/s, the matrix unit busy 51 % of its cycles at 2.0 GHz.  Timing copies without
+// the copies into LDS, or without the fragments' reads, take 379 and 298 us where the
+// whole took 490 (8192^3): both ways through LDS bound it, and the multiply-adds.
 //
 // KS groups of such waves share the steps (group i takes blocks i, i + KS, ...), each
 // with its own buffers, and their sums meet at the end, the first group's first: a
@@ -392,6 +396,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
 // workgroup has to have its share of them in flight at once.  A workgroup takes 16
 // columns and all of K, its W waves the blocks w, w + W, ...; fragments go from
 // memory straight into registers, and the waves' sums meet in LDS in their order.
+// 1 x 6192 x 2048: 4.1 us (3.1 TB/s); 1 x 8192 x 8192: 12.4 us (5.4 TB/s); 16 x 6192 x 2048:
+// 6.2 us.
 template <int TM, int W, typename Eo>
 __global__ __launch_bounds__(64 * W) void qgemm_few_kernel(GemmArgs p) {
     __shared__ float sum[W][TM][16][17];
