@@ -130,7 +130,7 @@ template <int N> __device__ __forceinline__ void step_wait() {
 // 16 rows a fragment reads at one k lie in different banks.  Rows behind the last one
 // of A or B are copies of it, whose products are not stored; pieces behind K are
 // zeros.
-// The one barrier of a step stands before the products of its last row of fragments:
+// The one barrier of a step stands before the products of its last rows of fragments:
 // by then everybody has read the step's operands, whose buffer is filled anew, and
 // has its part of the next step's, whose first fragments are read while those
 // products run.
