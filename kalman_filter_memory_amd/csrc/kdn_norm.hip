@@ -464,7 +464,7 @@ kdn_status kdn_quantize(const kdn_quant_desc* n, const void* x, void* q, float* 
     if (!type_ok(n->dtype) || (n->block_rows != 1 && n->block_rows != kdn::kQuantBlock))
         return KDN_ERR_UNSUPPORTED;
     if (n->d % 8 != 0 || n->rows > INT32_MAX) return KDN_ERR_UNSUPPORTED;
-    const int nb = (n->d + kdn::kQuantBlock - 1) / kdn::kQuantBlock;
+    const int nb = int((int64_t(n->d) + kdn::kQuantBlock - 1) / kdn::kQuantBlock);
     const int64_t br = (n->rows + n->block_rows - 1) / n->block_rows;
     const int64_t groups = n->block_rows == 1 ? (n->rows * nb + 15) / 16 : br * nb;
     if (groups > kMaxGroups) return KDN_ERR_UNSUPPORTED;

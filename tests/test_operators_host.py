@@ -82,6 +82,9 @@ QUANT_BAD = [
     (dict(rows=-1), 2), (dict(d=-8), 2), (dict(d=12), 3), (dict(block_rows=0), 3),
     (dict(block_rows=64), 3), (dict(dtype=9), 3), (dict(rows=1 << 33), 3),
     (dict(rows=(1 << 31) - 1, d=1024), 3),
+    # the last multiple of 8 below 2^31: 2^24 blocks, counted without passing 32 bits
+    (dict(rows=1, d=(1 << 31) - 8, block_rows=128), 3),
+    (dict(rows=16, d=(1 << 31) - 8), 3),
 ]
 
 
