@@ -45,10 +45,10 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red)
 
 // One row per TPR threads; thread t holds columns 8 (t + TPR v) .. + 7 of it.
 // 16 neighbouring threads hold one block of 128 columns, so its maximum is four
-// DPP steps.  A wave per row, up to 2048 columns, meets no barrier; wider rows
-// would not fit a wave's registers beside enough others to hide the loads.
-// 32768 x 2048 bfloat16 with residual to 8 bits: 93 us, 5.1 TB/s (what a copy of
-// this size reaches); 256 rows of it 4.4 us, 1537 x 2056 float32 10.8 us (4.7 TB/s).
+// DPP steps.  A wave per row, up to 1024 columns, meets no barrier; wider rows
+// would leave too few waves to hide the loads.
+// 32768 x 2048 bfloat16 with residual to 8 bits: 82 us, 5.8 TB/s (above what a copy
+// reaches, which writes more of its bytes); 256 rows of it 4.2 us, 1537 x 2056 float32 10.8 us (4.7 TB/s).
 template <typename Ex, typename Er, bool RES, bool QUANT, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
     int rows, int d, float eps, const Ex* __restrict__ x, const Er* residual,
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
 // of them and the workgroup writes one partial row of dw, which dw_kernel adds
 // up in a fixed order (no atomics: the same inputs give the same bits).  1024
 // workgroups fill the GPU four times and leave 8 MB of partial rows at 2048 columns.
-// 32768 x 2048 bfloat16: 156 us and 6 us for dw, 5.0 TB/s.
+// 32768 x 2048 bfloat16: 147 us and 6 us for dw, 5.3 TB/s.
 template <typename Ex, typename Er, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(
     int rows, int d, const Ex* __restrict__ dy, const Er* __restrict__ s,
@@ -313,7 +313,9 @@ kdn_status check_norm(const kdn_norm_desc* n) {
 }
 
 // Threads per row: a wave, while the row fits a wave's registers; more for wide rows.
-bool wave_rows(int d) { return d <= 2048; }
+// (the rule by both sides, to 8 bits and backward: 32768 x 2048 93 and 168 us with a wave,
+// 82 and 158 with four; 32768 x 1024 37 and 68 against 42 and 80)
+bool wave_rows(int d) { return d <= 1024; }
 
 struct NormArgs {
     int rows, d;
@@ -340,9 +342,9 @@ template <typename Ex, typename Er, bool RES, bool QUANT>
 void norm_width(const NormArgs& a, hipStream_t st) {
     if (wave_rows(a.d)) {
         if (a.d <= 512) return norm_launch<Ex, Er, RES, QUANT, 64, 1>(a, st);
-        if (a.d <= 1024) return norm_launch<Ex, Er, RES, QUANT, 64, 2>(a, st);
-        return norm_launch<Ex, Er, RES, QUANT, 64, 4>(a, st);
+        return norm_launch<Ex, Er, RES, QUANT, 64, 2>(a, st);
     }
+    if (a.d <= 2048) return norm_launch<Ex, Er, RES, QUANT, 256, 1>(a, st);
     if (a.d <= 4096) return norm_launch<Ex, Er, RES, QUANT, 256, 2>(a, st);
     if (a.d <= 8192) return norm_launch<Ex, Er, RES, QUANT, 256, 4>(a, st);
     return norm_launch<Ex, Er, RES, QUANT, 256, 8>(a, st);
@@ -403,9 +405,9 @@ void bwd_launch(const BwdNormArgs& a, hipStream_t st) {
 template <typename Ex, typename Er> void bwd_width(const BwdNormArgs& a, hipStream_t st) {
     if (wave_rows(a.d)) {
         if (a.d <= 512) return bwd_launch<Ex, Er, 64, 1>(a, st);
-        if (a.d <= 1024) return bwd_launch<Ex, Er, 64, 2>(a, st);
-        return bwd_launch<Ex, Er, 64, 4>(a, st);
+        return bwd_launch<Ex, Er, 64, 2>(a, st);
     }
+    if (a.d <= 2048) return bwd_launch<Ex, Er, 256, 1>(a, st);
     if (a.d <= 4096) return bwd_launch<Ex, Er, 256, 2>(a, st);
     if (a.d <= 8192) return bwd_launch<Ex, Er, 256, 4>(a, st);
     return bwd_launch<Ex, Er, 256, 8>(a, st);

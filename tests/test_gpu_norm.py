@@ -47,7 +47,7 @@ def _cuda(*xs):
 
 
 # rows, d, dtype, residual's dtype: one row, one vector, ragged blocks, a wave per
-# row up to 2048 columns and a workgroup per row beyond, the widest row
+# row up to 1024 columns and a workgroup per row beyond, the widest row
 SHAPES = [
     (1, 8, "f32", None), (1, 8, "bf16", "bf16"), (3, 64, "bf16", "f32"), (5, 120, "bf16", "bf16"),
     (7, 136, "f32", "f32"), (130, 512, "bf16", None), (9, 520, "bf16", "f32"), (2, 1024, "f32", "f32"),
@@ -181,7 +181,7 @@ def test_norm_backward_matches_the_formula(shape, with_ds):
                + (0 if ds is None else 2 * ds.abs().double()))
     assert ((dx.cpu().double() - dx0).abs() <= tol).all()
     t = dy.double() * xh
-    rpb = 4 if d <= 2048 else 1
+    rpb = 4 if d <= 1024 else 1  # rows of a workgroup
     groups = min(-(-rows // rpb), 1024)
     steps = -(-rows // (groups * rpb)) + 3 + -(-groups // 128) + 7 + 3
     assert ((dw.cpu().double() - t.sum(0)).abs() <= steps * U * t.abs().sum(0)).all()
