@@ -47,7 +47,7 @@ def _inputs(B, H, T, d, dtype, gate, seed, kind="decay"):
 
 
 # B, H, T, d, x's type, a's type.  Tiles are 64 to 1024 tokens: one token, less than
-# a strip, one tile, a few tiles and several groups of eight tiles in a chain, two
+# a strip, one tile, a few tiles and several groups of tiles in a chain, two
 # channel blocks, and so many sequences that a workgroup walks along its own.
 SHAPES = [
     (1, 1, 1, 8, "f32", "f32"), (2, 3, 5, 32, "bf16", "bf16"), (1, 2, 257, 64, "bf16", "f32"),
