@@ -81,9 +81,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
     for (int v = 0; v < NV; ++v) {
         const int c = 8 * (t + TPR * v);
         if constexpr (RES) {
-            // (not read again before the layer behind this norm is done; 32768 x 2048
-            // bfloat16: 94 -> 89.5 us)
-            if (c < d) kdn::store8<Er, true>(s_out + base + c, s[v]);
+            if (c < d) kdn::store8<Er>(s_out + base + c, s[v]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(s[v][i], s[v][i], ss);

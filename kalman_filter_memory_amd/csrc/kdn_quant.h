@@ -47,21 +47,17 @@ __device__ __forceinline__ u32x2 quant8(const float* x, float inv) {
     return u32x2{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
 }
 
-__device__ __forceinline__ void store16(u32x4* p, u32x4 v, bool stream) {
-    if (stream) __builtin_nontemporal_store(v, p);
-    else *p = v;
-}
-// eight floats at p (16-byte aligned) in E; STREAM: written past the caches
-template <typename E, bool STREAM = false> __device__ __forceinline__ void store8(E* p, const float* f) {
+// eight floats at p (16-byte aligned) in E
+template <typename E> __device__ __forceinline__ void store8(E* p, const float* f) {
     u32x4* o = reinterpret_cast<u32x4*>(p);
     if constexpr (sizeof(E) == 2) {
-        store16(o, u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                         pack_bf16(f[6], f[7])}, STREAM);
+        *o = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                   pack_bf16(f[6], f[7])};
     } else {
-        store16(o, u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                         __float_as_uint(f[3])}, STREAM);
-        store16(o + 1, u32x4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                             __float_as_uint(f[7])}, STREAM);
+        o[0] = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3])};
+        o[1] = u32x4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                     __float_as_uint(f[7])};
     }
 }
 
