@@ -332,16 +332,19 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
     for (; (k + S + 1) * KS <= full; ++k) step(k, std::false_type{});
     for (; k < steps; ++k) step(k, std::true_type{});
     if constexpr (KS > 1) {
-        static_assert(KS == 2 && BM * BN * 4 <= int(sizeof(tiles)), "two groups");
+        static_assert((KS - 1) * BM * BN * 4 <= int(sizeof(tiles)), "the groups' sums fit the operands' place");
         floatx4* sums = reinterpret_cast<floatx4*>(&tiles[0][0][0]);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TM * TN; ++i)
-            if (grp == 1) sums[(i * W + wave) * 64 + lane] = acc[i / TN][i % TN];
+            if (grp > 0) sums[((grp - 1) * TM * TN * W + i * W + wave) * 64 + lane] = acc[i / TN][i % TN];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < TM * TN; ++i)
-            if (grp == 0) acc[i / TN][i % TN] += sums[(i * W + wave) * 64 + lane];
+            if (grp == 0)
+#pragma unroll
+                for (int o = 0; o < KS - 1; ++o)
+                    acc[i / TN][i % TN] += sums[(o * TM * TN * W + i * W + wave) * 64 + lane];
     }
     // C goes through LDS, rounded, so that a wave writes whole rows of the tile: written
     // from the fragments, 64 bytes of 16 rows at a time, rows that do not start on a
@@ -349,8 +352,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
     // 453 against 397 us for rows of 6208).  Pieces of a row are stored in an order that
     // depends on the row, as above.
     constexpr int V = 16 / int(sizeof(Eo)), CR = BN / V;  // columns, and pieces of a row
-    static_assert(BM * CR * 16 <= int(sizeof(tiles)) && CR >= 8, "C fits the operands' place");
-    auto key_c = [](int r) { return CR >= 16 ? r & 15 : (r >> 1) & 7; };
+    static_assert(BM * CR * 16 <= int(sizeof(tiles)) && CR >= 4, "C fits the operands' place");
+    auto key_c = [](int r) { return CR >= 16 ? r & 15 : CR >= 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
     u32x4* out = reinterpret_cast<u32x4*>(&tiles[0][0][0]);
     __syncthreads();
 #pragma unroll
@@ -372,21 +375,52 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
         }
     }
     __syncthreads();
+    constexpr int NT = 64 * W * KS;
+    if (p.wide) {
 #pragma unroll 4
-    for (int o = threadIdx.x; o < BM * CR; o += 64 * W * KS) {
-        const int r = o / CR, c = o % CR, m = m0 + r, n = n0 + c * V;
-        const u32x4 u = out[r * CR + (c ^ key_c(r))];
-        if (m < p.M && n < p.N) {
-            Eo* row = static_cast<Eo*>(p.C) + size_t(m) * p.ldc;
-            if (p.wide && n + V <= p.N) {
-                *reinterpret_cast<u32x4*>(row + n) = u;
+        for (int o = threadIdx.x; o < BM * CR; o += NT) {
+            const int r = o / CR, c = o % CR, m = m0 + r, n = n0 + c * V;
+            const u32x4 u = out[r * CR + (c ^ key_c(r))];
+            if (m < p.M && n < p.N) {
+                Eo* row = static_cast<Eo*>(p.C) + size_t(m) * p.ldc;
+                if (n + V <= p.N) {
+                    *reinterpret_cast<u32x4*>(row + n) = u;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (n + e < p.N) {
+                            if constexpr (sizeof(Eo) == 2) row[n + e] = bf16_t(u[e / 2] >> (16 * (e & 1)));
+                            else row[n + e] = __uint_as_float(u[e]);
+                        }
+                }
+            }
+        }
+    } else {
+        // rows that start anywhere: the pieces are those of memory, aligned there, and
+        // are put together from the row's elements (one more piece: the first and the
+        // last are parts).  8192 x 4097 x 1024 bfloat16 86 us with the tile's own pieces,
+        // written in elements, 67 so; 25230 x 3861 x 64 float32 151 and 119.
+        const Eo* el = reinterpret_cast<const Eo*>(out);
+        for (int o = threadIdx.x; o < BM * (CR + 1); o += NT) {
+            const int r = o / (CR + 1), m = m0 + r;
+            if (m >= p.M) continue;
+            Eo* row = static_cast<Eo*>(p.C) + size_t(m) * p.ldc + n0;
+            const int c = (o % (CR + 1)) * V - int(uintptr_t(row) / sizeof(Eo) % V);
+            const int end = p.N - n0 < BN ? p.N - n0 : BN;
+            Eo v[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int col = c + e < 0 ? 0 : c + e < BN ? c + e : BN - 1;
+                v[e] = el[(r * CR + ((col / V) ^ key_c(r))) * V + col % V];
+            }
+            if (c >= 0 && c + V <= end) {
+                u32x4 u;
+                __builtin_memcpy(&u, v, 16);
+                *reinterpret_cast<u32x4*>(row + c) = u;
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    if (n + e < p.N) {
-                        if constexpr (sizeof(Eo) == 2) row[n + e] = bf16_t(u[e / 2] >> (16 * (e & 1)));
-                        else row[n + e] = __uint_as_float(u[e]);
-                    }
+                    if (c + e >= 0 && c + e < end) row[c + e] = v[e];
             }
         }
     }
@@ -396,8 +430,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
 // workgroup has to have its share of them in flight at once.  A workgroup takes 16
 // columns and all of K, its W waves the blocks w, w + W, ...; fragments go from
 // memory straight into registers, and the waves' sums meet in LDS in their order.
-// 1 x 6192 x 2048: 4.1 us (3.1 TB/s); 1 x 8192 x 8192: 12.4 us (5.4 TB/s); 16 x 6192 x 2048:
-// 6.2 us.
+// 1 x 6192 x 2048: 4.1 us (3.1 TB/s); 1 x 8192 x 8192: 12.8 us (5.2 TB/s); 16 x 2048 x 2048:
+// 4.0 us.
 template <int TM, int W, typename Eo>
 __global__ __launch_bounds__(64 * W) void qgemm_few_kernel(GemmArgs p) {
     __shared__ float sum[W][TM][16][17];
@@ -475,12 +509,15 @@ template <int BM, int BN, int WM, int WN, int S, int KS, typename Eo> void launc
 
 template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
     const unsigned cols = unsigned((a.N + 15) / 16);
-    // Up to 32 rows: 32 x 2048 x 8192 takes 16.3 us against 21.0 in tiles of 64 x 64, 16 x
-    // 8192 x 8192 19.8 against 34.0; at 48 x 6192 x 2048 the tiles are ahead, 7.4 against
-    // 12.5 with three times 16 rows.
-    if (a.M <= 16) {
+    // Few rows, and no more than one workgroup per CU: 16 x 2048 x 2048 takes 4.0 us against
+    // 4.9 in tiles of 32 x 32, 12 x 4096 x 4096 6.0 against 6.4, but 16 x 6192 x 2048 6.3
+    // against 4.9 and 16 x 8192 x 8192 19.5 against 15.2, for every
+    // workgroup reads every row of A.  Up to four rows are ahead anywhere (4 x 8192 x 8192 13.9 against 15.0, 1 row
+    // 12.8 against 14.9), 17 to 32 with a short K (24 x 1000 x 1024 3.5 against 4.2; 32 x
+    // 2048 x 2048 5.5 against 4.9).
+    if (a.M <= 4 || (a.M <= 16 && cols <= 256)) {
         qgemm_few_kernel<1, 8, Eo><<<cols, 512, 0, st>>>(a);
-    } else if (a.M <= 32) {
+    } else if (a.M <= 32 && cols <= 256 && a.kb <= 8) {
         qgemm_few_kernel<2, 8, Eo><<<cols, 512, 0, st>>>(a);
     } else {
         // The larger the tile, the less is read per product, as long as the tiles fill
@@ -490,10 +527,16 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         // 63.1, 3000 x 6192 (300, two rounds) 66.0 against 53.4.  Against 64 x 64: 512 x
         // 6192 is 196 tiles of 128 x 128 and takes 13.4 in them against 15.7, 1024 x 2048
         // is 128 and takes 11.8 against 9.9.  (Widened operands leave no registers for
-        // the largest tile.)  Two groups of waves per 64 x 64 tile while all tiles run at
-        // once, two to a CU, and K is long enough: 256 x 2048 x 2048 7.3 -> 6.8 (float32
-        // 10.4 -> 9.0), 509 x 2048 x 2064 8.8 -> 8.6 (11.8 -> 10.7); but 384 x 6192 x 2048,
-        // 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8.
+        // the largest tile.)  With fewer tiles than fill the GPU groups of waves
+        // share K, if it is long enough: two groups per 64 x 64 tile while all tiles run at
+        // once, two to a CU (509 x 2048 x 2064 8.8 -> 8.2, float32 11.8 -> 10.3; but 384 x
+        // 6192 x 2048, 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8), four of
+        // them one to a CU where K is longer (256 x 4096 x 8192 24.5 -> 20.4, x 4096 in
+        // float32 14.5 -> 14.1; x 2048 7.1 -> 7.9), and four per 32 x 32 tile while those
+        // run at once, two to a CU (64 x 6192 x 2048 6.7 -> 5.9, 128 x 2048 x 8192 16.8 ->
+        // 9.8, 430 x 270 x 4576 in float32 16.1 -> 9.0; 256 x 4096 x 2048, 1024 such tiles,
+        // 7.1 -> 10.6).
+        const int64_t tiny = int64_t((a.M + 31) / 32) * ((a.N + 31) / 32);
         const int64_t few = int64_t((a.M + 63) / 64) * ((a.N + 63) / 64);
         const int64_t big = int64_t((a.M + 255) / 256) * ((a.N + 255) / 256);
         const int64_t mid = int64_t((a.M + 127) / 128) * ((a.N + 127) / 128);
@@ -501,6 +544,10 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
             launch_tiles<256, 256, 2, 4, 2, 1, bf16_t>(a, st);
         else if (mid >= 192)
             launch_tiles<128, 128, 2, 2, 2, 1, Eo>(a, st);
+        else if (a.kb >= 8 && tiny <= 512)
+            launch_tiles<32, 32, 1, 1, 2, 4, Eo>(a, st);
+        else if (a.kb >= 32 && few <= 256)
+            launch_tiles<64, 64, 2, 2, 2, 4, Eo>(a, st);
         else if (a.kb >= 8 && few <= 512)
             launch_tiles<64, 64, 2, 2, 2, 2, Eo>(a, st);
         else

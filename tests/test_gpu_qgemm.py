@@ -61,6 +61,8 @@ SHAPES = [
     (128, 128, 128), (129, 1, 384), (257, 513, 640), (509, 2048, 2064), (2000, 2100, 400),
     (40, 70, 1024), (200, 300, 1040), (300, 190, 1168), (64, 64, 3200), (448, 4000, 2048), (450, 4100, 1040),
     (2048, 2048, 2048), (4095, 4100, 1168), (4096, 4096, 256), (70, 6192, 2048), (5000, 24, 96),
+    (4, 4500, 1040), (7, 4500, 1040), (8, 5000, 272), (20, 130, 1040), (40, 6001, 2064), (257, 2100, 4112),
+    (4090, 4093, 144), (4096, 4095, 272),
 ]
 
 
