@@ -26,10 +26,15 @@
 // bits.  A workgroup takes its tile from a counter, in an order in which a tile
 // comes after everything it waits for: whoever holds an earlier tile is already
 // running and waits for earlier tiles only, so every wait ends.
-// The rule: a chain where the (sequence, channel block) pairs are fewer than 1024, four
-// to a CU (B1 H16 T65536 d128 bfloat16 has 16 and runs at 5.2 TB/s in 154 us with its
-// 5.5 us of clearing the chain; the backward of B8 H16 T4096 has 128 and takes 188 us,
-// 5.0 TB/s); beyond, the pairs alone fill the GPU.
+// The rule: the walk where it has two tiles at most, where the pairs are 1024 or more, four
+// to a CU, and where they leave few of the 256 CUs idle in their last round: a tile is
+// 200 KB, 10 us of a CU's share of the memory's time, and the chain's clearing and waits
+// cost 6 us, 0.6 of that, so the walk is ahead up to 160 idle CU tiles.  (us, with walk and
+// chain: 256 x 300 x 128 bfloat16 14.6, 21.3, x 4000 142, 144, the backward in float32 564,
+// 627; 215 x 335 x 128 float32 28.4, 34.5; 16 x 200 x 128 float32 backward, two tiles, 10.1,
+// 13.6; but 406 pairs of 826 tokens in float32 123, 106, 64 x 1000 x 128 bfloat16 24.3,
+// 16.5.)  B1 H16 T65536 d128 bfloat16, a chain, runs at 5.2 TB/s in 154 us with its 5.5 us
+// of clearing; the backward of B8 H16 T4096 takes 188 us, 5.0 TB/s.
 // A published word is one atomic access whose value cannot be the mark "not yet
 // there" (all bits set), so it needs no flag and no fence.
 #include <hip/hip_runtime.h>
@@ -50,7 +55,6 @@ constexpr int kGroup = 16;
 constexpr int kMaxGroups = (1 << 24) - 1;  // a grid holds fewer than 2^32 threads
 constexpr uint32_t kNotYet = 0xffffffffu;
 constexpr uint32_t kNaN = 0x7fc00000u;
-
 
 // 8 channels as loaded: 4 or 8 words
 template <typename E> struct Vec8 {
@@ -367,7 +371,8 @@ Plan plan_of(const kdn_scan_desc* s, bool bwd) {
     p.tile = kThreads / p.lanes * p.L;
     p.nt = int((int64_t(s->T) + p.tile - 1) / p.tile);
     p.nblk = (s->d + 8 * p.lanes - 1) / (8 * p.lanes);
-    p.chain = p.nt > 1 && int64_t(p.seqs) * p.nblk < 1024;
+    const int64_t pairs = int64_t(p.seqs) * p.nblk, idle = (256 - pairs % 256) % 256;
+    p.chain = p.nt > 2 && pairs < 1024 && p.nt * idle > 160;
     p.total = 16;
     if (p.chain) {
         const size_t ng = (p.nt + kGroup - 1) / kGroup;

@@ -48,12 +48,14 @@ def _inputs(B, H, T, d, dtype, gate, seed, kind="decay"):
 
 # B, H, T, d, x's type, a's type.  Tiles are 64 to 1024 tokens: one token, less than
 # a strip, one tile, a few tiles and several groups of tiles in a chain, two
-# channel blocks, and so many sequences that a workgroup walks along its own.
+# channel blocks, and as many sequences as CUs or more, so that a workgroup walks along
+# its own.
 SHAPES = [
     (1, 1, 1, 8, "f32", "f32"), (2, 3, 5, 32, "bf16", "bf16"), (1, 2, 257, 64, "bf16", "f32"),
     (1, 1, 4500, 128, "bf16", "bf16"), (2, 1, 2100, 200, "f32", "bf16"), (1, 1, 9000, 32, "bf16", "bf16"),
     (1, 1, 9000, 24, "f32", "f32"), (3, 1, 1024, 128, "bf16", "bf16"), (1, 2, 1025, 128, "f32", "f32"),
     (64, 16, 300, 128, "bf16", "bf16"), (512, 2, 530, 40, "bf16", "f32"), (1, 1, 700, 1000, "bf16", "bf16"),
+    (250, 1, 700, 72, "bf16", "f32"), (3, 1, 400, 128, "f32", "f32"),
 ]
 IDS = ["-".join(map(str, s)) for s in SHAPES]
 
