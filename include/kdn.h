@@ -526,7 +526,7 @@ typedef struct {
 } kdn_scan_desc;
 
 /* Bytes of workspace kdn_gated_scan / kdn_gated_scan_backward need (0 if the
- * descriptor is invalid).  Host-only. */
+ * descriptor is invalid; 16: none, ws may be NULL).  Host-only. */
 size_t kdn_gated_scan_workspace_bytes(const kdn_scan_desc *s);
 size_t kdn_gated_scan_backward_workspace_bytes(const kdn_scan_desc *s);
 

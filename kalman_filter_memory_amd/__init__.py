@@ -910,9 +910,9 @@ def gated_scan(x, a, h0=None):
     need = load_library().kdn_gated_scan_workspace_bytes(ctypes.byref(s))
     h = torch.empty_like(x)
     h_T = _empty((B, H, d), torch.float32, dev)
-    ws = _empty((max(need, 16),), torch.uint8, dev)
+    ws = _empty((need,), torch.uint8, dev) if need > 16 else None
     _launch("kdn_gated_scan", dev, ctypes.byref(s), _ptr(x), _ptr(a), _ptr(h0), _ptr(h),
-            _ptr(h_T), _ptr(ws), ws.numel())
+            _ptr(h_T), _ptr(ws), need)
     return h, h_T
 
 
@@ -931,9 +931,9 @@ def gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict:
     need = load_library().kdn_gated_scan_backward_workspace_bytes(ctypes.byref(s))
     g = {n: torch.empty_like(h, dtype=torch.float32) for n in ("dx", "da")}
     g["dh0"] = _empty((B, H, d), torch.float32, dev)
-    ws = _empty((max(need, 16),), torch.uint8, dev)
+    ws = _empty((need,), torch.uint8, dev) if need > 16 else None
     _launch("kdn_gated_scan_backward", dev, ctypes.byref(s), _ptr(a), _ptr(h), _ptr(h0), _ptr(dh),
-            _ptr(dh_T), _ptr(g["dx"]), _ptr(g["da"]), _ptr(g["dh0"]), _ptr(ws), ws.numel())
+            _ptr(dh_T), _ptr(g["dx"]), _ptr(g["da"]), _ptr(g["dh0"]), _ptr(ws), need)
     return g
 
 

@@ -360,7 +360,7 @@ constexpr int strip(bool f32, bool bwd) { return f32 || bwd ? 8 : 16; }
 struct Plan {
     int seqs, lanes, L, tile, nt, nblk;
     bool chain;
-    size_t agg, start, total;  // byte offsets in the workspace; total at least 16
+    size_t start, total;  // byte offsets in the workspace; total 16 without a chain
 };
 
 Plan plan_of(const kdn_scan_desc* s, bool bwd) {
@@ -467,8 +467,8 @@ kdn_status kdn_gated_scan(const kdn_scan_desc* s, const void* x, const void* a, 
     for (const void* q : {x, a, (const void*)h0, (const void*)h, (const void*)h_T, (const void*)ws})
         if (!aligned16(q)) return KDN_ERR_ALIGN;
     if (s->T == 0) return pass_through(s, h0, h_T, hs);
-    if (!x || !a || !h || !ws) return KDN_ERR_NULL;
-    if (ws_bytes < p.total) return KDN_ERR_WORKSPACE;
+    if (!x || !a || !h || (p.chain && !ws)) return KDN_ERR_NULL;
+    if (p.chain && ws_bytes < p.total) return KDN_ERR_WORKSPACE;
     ScanArgs g{};
     g.a = a;
     g.x = x;
@@ -491,8 +491,8 @@ kdn_status kdn_gated_scan_backward(const kdn_scan_desc* s, const void* a, const 
                           (const void*)da, (const void*)dh0, (const void*)ws})
         if (!aligned16(q)) return KDN_ERR_ALIGN;
     if (s->T == 0) return pass_through(s, dh_T, dh0, hs);
-    if (!a || !h || !dh || !dx || !da || !ws) return KDN_ERR_NULL;
-    if (ws_bytes < p.total) return KDN_ERR_WORKSPACE;
+    if (!a || !h || !dh || !dx || !da || (p.chain && !ws)) return KDN_ERR_NULL;
+    if (p.chain && ws_bytes < p.total) return KDN_ERR_WORKSPACE;
     ScanArgs g{};
     g.a = a;
     g.x = dh;

@@ -151,6 +151,10 @@ def test_scan_refuses_arguments(lib):
         assert lib.kdn_gated_scan_backward(s, *args, back, None) == 5
     assert lib.kdn_gated_scan_backward(s, *([FAKE] * 9), back - 1, None) == 4
     assert lib.kdn_gated_scan(ctypes.byref(_scan(B=0)), *([None] * 6), 0, None) == 0
+    # one tile, or two: no workspace
+    assert lib.kdn_gated_scan_backward_workspace_bytes(ctypes.byref(_scan())) == 16
+    assert lib.kdn_gated_scan_workspace_bytes(ctypes.byref(_scan(T=2048))) > 16
+    assert lib.kdn_gated_scan_workspace_bytes(ctypes.byref(_scan(T=512))) == 16
     step = lib.kdn_gated_scan_step
     for i in (0, 1, 2):
         args = [FAKE] * 4
