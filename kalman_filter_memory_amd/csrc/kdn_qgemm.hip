@@ -396,32 +396,42 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
             }
         }
     } else {
-        // rows that start anywhere: the pieces are those of memory, aligned there, and
-        // are put together from the row's elements (one more piece: the first and the
-        // last are parts).  8192 x 4097 x 1024 bfloat16 86 us with the tile's own pieces,
-        // written in elements, 67 so; 25230 x 3861 x 64 float32 151 and 119.
+        // Rows that start anywhere: the pieces are those of memory, aligned there, each
+        // from two neighbours of the tile's, and what is left at the row's two ends is
+        // written in elements.  8192 x 4097 x 1024 bfloat16 86 us with the tile's own
+        // pieces, written in elements, 55 so; 25230 x 3861 x 64 float32 151 and 90.
+        const int end = p.N - n0 < BN ? p.N - n0 : BN;
+        // the first column of row m that is aligned
+        auto first = [&](int m) { return int((0u - uint32_t(m) * uint32_t(p.ldc)) & (V - 1)); };
+#pragma unroll 2
+        for (int o = threadIdx.x; o < BM * CR; o += NT) {
+            const int r = o / CR, c = o % CR, m = m0 + r, off = first(m), n = c * V + off;
+            const u32x4 lo = out[r * CR + (c ^ key_c(r))];
+            const u32x4 hi = out[r * CR + ((c + 1 < CR ? c + 1 : c) ^ key_c(r))];
+            const int words = off * int(sizeof(Eo)) / 4;
+            const bool two = words & 2, one = words & 1, half = sizeof(Eo) == 2 && (off & 1);
+            // (by value: a choice between two elements of an array would be one of their
+            // addresses, and the array in memory)
+            auto pick = [](bool x, uint32_t a, uint32_t b) { return x ? a : b; };
+            uint32_t w[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = pick(two, w[i + 2], w[i]);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = pick(one, w[i + 1], w[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pick(half, (w[i] >> 16) | (w[i + 1] << 16), w[i]);
+            if (m < p.M && n + V <= end)
+                *reinterpret_cast<u32x4*>(static_cast<Eo*>(p.C) + size_t(m) * p.ldc + n0 + n) =
+                    u32x4{w[0], w[1], w[2], w[3]};
+        }
         const Eo* el = reinterpret_cast<const Eo*>(out);
-        for (int o = threadIdx.x; o < BM * (CR + 1); o += NT) {
-            const int r = o / (CR + 1), m = m0 + r;
-            if (m >= p.M) continue;
-            Eo* row = static_cast<Eo*>(p.C) + size_t(m) * p.ldc + n0;
-            const int c = (o % (CR + 1)) * V - int(uintptr_t(row) / sizeof(Eo) % V);
-            const int end = p.N - n0 < BN ? p.N - n0 : BN;
-            Eo v[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int col = c + e < 0 ? 0 : c + e < BN ? c + e : BN - 1;
-                v[e] = el[(r * CR + ((col / V) ^ key_c(r))) * V + col % V];
-            }
-            if (c >= 0 && c + V <= end) {
-                u32x4 u;
-                __builtin_memcpy(&u, v, 16);
-                *reinterpret_cast<u32x4*>(row + c) = u;
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    if (c + e >= 0 && c + e < end) row[c + e] = v[e];
-            }
+        for (int o = threadIdx.x; o < BM * 2 * V; o += NT) {
+            const int r = o / (2 * V), e = o % (2 * V), m = m0 + r, off = first(m);
+            const int tail = off + (end > off ? (end - off) / V * V : 0);
+            const int c = e < V ? e : tail + e - V;
+            if (m < p.M && c < (e < V && off < end ? off : end))
+                static_cast<Eo*>(p.C)[size_t(m) * p.ldc + n0 + c] =
+                    el[(r * CR + ((c / V) ^ key_c(r))) * V + c % V];
         }
     }
 }
@@ -530,9 +540,10 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         // the largest tile.)  With fewer tiles than fill the GPU groups of waves
         // share K, if it is long enough: two groups per 64 x 64 tile while all tiles run at
         // once, two to a CU (509 x 2048 x 2064 8.8 -> 8.2, float32 11.8 -> 10.3; but 384 x
-        // 6192 x 2048, 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8), four of
-        // them one to a CU where K is longer (256 x 4096 x 8192 24.5 -> 20.4, x 4096 in
-        // float32 14.5 -> 14.1; x 2048 7.1 -> 7.9), and four per 32 x 32 tile while those
+        // 6192 x 2048, 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8), one to a
+        // CU with four steps in LDS, or in float32 with four groups, where K is longer (256 x
+        // 4096 x 8192 24.5 -> 18.5, x 4096 in float32 14.5 -> 14.1; 509 x 2048 x 2064 8.2 ->
+        // 8.4), and four per 32 x 32 tile while those
         // run at once, two to a CU (64 x 6192 x 2048 6.7 -> 5.9, 128 x 2048 x 8192 16.8 ->
         // 9.8, 430 x 270 x 4576 in float32 16.1 -> 9.0; 256 x 4096 x 2048, 1024 such tiles,
         // 7.1 -> 10.6).
@@ -547,7 +558,7 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         else if (a.kb >= 8 && tiny <= 512)
             launch_tiles<32, 32, 1, 1, 2, 4, Eo>(a, st);
         else if (a.kb >= 32 && few <= 256)
-            launch_tiles<64, 64, 2, 2, 2, 4, Eo>(a, st);
+            launch_tiles<64, 64, 2, 2, sizeof(Eo) == 2 ? 4 : 2, sizeof(Eo) == 2 ? 2 : 4, Eo>(a, st);
         else if (a.kb >= 8 && few <= 512)
             launch_tiles<64, 64, 2, 2, 2, 2, Eo>(a, st);
         else
