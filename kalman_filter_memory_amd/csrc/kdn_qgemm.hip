@@ -537,16 +537,16 @@ template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
         // 63.1, 3000 x 6192 (300, two rounds) 66.0 against 53.4.  Against 64 x 64: 512 x
         // 6192 is 196 tiles of 128 x 128 and takes 13.4 in them against 15.7, 1024 x 2048
         // is 128 and takes 11.8 against 9.9.  (Widened operands leave no registers for
-        // the largest tile.)  With fewer tiles than fill the GPU groups of waves
-        // share K, if it is long enough: two groups per 64 x 64 tile while all tiles run at
-        // once, two to a CU (509 x 2048 x 2064 8.8 -> 8.2, float32 11.8 -> 10.3; but 384 x
-        // 6192 x 2048, 582 tiles, 12.5 -> 15.5, and 100 x 1000 x 128 3.1 -> 3.8), one to a
-        // CU with four steps in LDS, or in float32 with four groups, where K is longer (256 x
-        // 4096 x 8192 24.5 -> 18.5, x 4096 in float32 14.5 -> 14.1; 509 x 2048 x 2064 8.2 ->
-        // 8.4), and four per 32 x 32 tile while those
-        // run at once, two to a CU (64 x 6192 x 2048 6.7 -> 5.9, 128 x 2048 x 8192 16.8 ->
-        // 9.8, 430 x 270 x 4576 in float32 16.1 -> 9.0; 256 x 4096 x 2048, 1024 such tiles,
-        // 7.1 -> 10.6).
+        // the largest tile.)
+        // With fewer tiles than fill the GPU groups of waves share K, if it is long enough:
+        // two groups per 64 x 64 tile while all tiles run at once, two to a CU (509 x 2048 x
+        // 2064 8.8 -> 8.2, float32 11.8 -> 10.3; but 384 x 6192 x 2048, 582 tiles, 12.5 ->
+        // 15.5, and 100 x 1000 x 128 3.1 -> 3.8); one to a CU with four steps in LDS, or in
+        // float32 with four groups, where K is longer (256 x 4096 x 8192 24.5 -> 18.5, x 4096
+        // in float32 14.5 -> 14.1; 509 x 2048 x 2064 8.2 -> 8.4); four groups per 32 x 32 tile
+        // while those run at once, two to a CU (64 x 6192 x 2048 6.7 -> 5.9, 128 x 2048 x
+        // 8192 16.8 -> 9.8, 430 x 270 x 4576 in float32 16.1 -> 9.0; 256 x 4096 x 2048, 1024
+        // such tiles, 7.1 -> 10.6).
         const int64_t tiny = int64_t((a.M + 31) / 32) * ((a.N + 31) / 32);
         const int64_t few = int64_t((a.M + 63) / 64) * ((a.N + 63) / 64);
         const int64_t big = int64_t((a.M + 255) / 256) * ((a.N + 255) / 256);

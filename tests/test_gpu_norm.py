@@ -182,7 +182,8 @@ def test_norm_backward_matches_the_formula(shape, with_ds):
     assert ((dx.cpu().double() - dx0).abs() <= tol).all()
     t = dy.double() * xh
     rpb = 4 if d <= 1024 else 1  # rows of a workgroup
-    groups = min(-(-rows // rpb), 1024)
+    units = -(-rows // rpb)
+    groups = min(units, 512 if units < 4096 else 1024)
     steps = -(-rows // (groups * rpb)) + 3 + -(-groups // 128) + 7 + 3
     assert ((dw.cpu().double() - t.sum(0)).abs() <= steps * U * t.abs().sum(0)).all()
     again = kdn.rms_norm_backward(*args)
