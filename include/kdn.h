@@ -407,9 +407,11 @@ kdn_status kdn_backward_kept_events(const kdn_desc *d, const void *q, const void
  * The 8-bit format: e4m3 without infinities (largest value 448), with one
  * float32 scale per block of 128 columns of one row (activations) or per block
  * of 128 x 128 (weights); the last block of a row or column may be shorter.
- * value = element * scale, scale = max(max |value| / 448, 2^-126), and elements
- * are rounded to nearest even.  A block that holds a NaN has a NaN scale, one
- * that holds an infinity an infinite scale. */
+ * In float32: scale = max(max |value| * (1 / 448), 2^-126) with the rounded
+ * 1 / 448, and element = value / scale, rounded to nearest even; what an element
+ * stands for is element * scale.  (The same bits as torch's
+ * (x / (amax / 448.0).clamp_min(2**-126)).to(float8_e4m3fn) on this GPU.)  A block
+ * that holds a NaN has a NaN scale, one that holds an infinity an infinite scale. */
 
 /* rows x d, dense rows.  dtype: x, y and dy; residual_dtype: residual and s
  * (KDN_F32 or dtype).  d a multiple of 8 up to 16384, rows up to 2^24 - 1

@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256) void layer_out_quant_kernel(const E* __restric
         for (int i = 0; i < 8; ++i) m = kdn::umax(m, kdn::abs_bits(f[i]));
         const float sc = kdn::quant_scale(kdn::row_umax(m));
         if (c < n)
-            *reinterpret_cast<kdn::u32x2*>(q + size_t(row) * n + c) = kdn::quant8(f, 1.f / sc);
+            *reinterpret_cast<kdn::u32x2*>(q + size_t(row) * n + c) = kdn::quant8(f, 1.0 / sc);
         if (l16 == 0) scale[size_t(row) * nb + blk] = sc;
     }
 }

@@ -3,7 +3,7 @@
 //
 //   s = round(x + residual)          (the residual stream, in its own type)
 //   rstd = (mean_j s_j^2 + eps)^(-1/2),   y = s rstd w
-//   8 bits: per 128 columns scale = max(max |y| / 448, 2^-126), q = e4m3(y / scale)
+//   8 bits: per 128 columns scale = max(max |y| (1 / 448), 2^-126), q = e4m3(y / scale)
 // The norm is taken of s as stored, so that the backward, which reads the
 // stored s, differentiates exactly what was computed; y is rounded once, from
 // float32, also on its way to 8 bits.
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
             m = kdn::row_umax(in ? m : 0u);
             const float sc = kdn::quant_scale(m);
             if (in) {
-                *reinterpret_cast<kdn::u32x2*>(q + base + c) = kdn::quant8(f, 1.f / sc);
+                *reinterpret_cast<kdn::u32x2*>(q + base + c) = kdn::quant8(f, 1.0 / sc);
                 if ((t & 15) == 0)
                     scale[size_t(row) * ((d + kdn::kQuantBlock - 1) / kdn::kQuantBlock) +
                           c / kdn::kQuantBlock] = sc;
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(1024) void dw_kernel(int n, int d, const float* __r
 
 // x in 8 bits with a scale per 128 columns of one row: 16 lanes per block, one block
 // per lane group, so that many workgroups hide the loads.  4099 x 2056 bfloat16:
-// 5.3 us (4.8 TB/s).
+// 6.1 us (4.2 TB/s).
 template <typename E>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     size_t nblocks, int nb, int d, const E* __restrict__ x, uint8_t* __restrict__ q,
@@ -254,13 +254,13 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = kdn::umax(m, kdn::abs_bits(f[i]));
     const float sc = kdn::quant_scale(kdn::row_umax(m));
-    if (in) *reinterpret_cast<kdn::u32x2*>(q + row * d + c) = kdn::quant8(f, 1.f / sc);
+    if (in) *reinterpret_cast<kdn::u32x2*>(q + row * d + c) = kdn::quant8(f, 1.0 / sc);
     if (live && l16 == 0) scale[blk] = sc;
 }
 
 // the same with a scale per 128 x 128 block: one workgroup per block, the
 // block's 8 vectors per thread held in registers between maximum and rounding.
-// 6192 x 2048 bfloat16: 7.1 us (5.4 TB/s) in 784 workgroups.
+// 6192 x 2048 bfloat16: 8.0 us (4.8 TB/s) in 784 workgroups.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void quantize_block_kernel(
     int rows, int nb, int d, const E* __restrict__ x, uint8_t* __restrict__ q,
@@ -287,7 +287,8 @@ __global__ __launch_bounds__(kThreads) void quantize_block_kernel(
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
     m = kdn::umax(kdn::umax(red[0], red[1]), kdn::umax(red[2], red[3]));
-    const float sc = kdn::quant_scale(m), inv = 1.f / sc;
+    const float sc = kdn::quant_scale(m);
+    const double inv = 1.0 / sc;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const int64_t row = int64_t(br) * kdn::kQuantBlock + r0 + 16 * k;
