@@ -475,8 +475,15 @@ kdn_status kdn_quantize(const kdn_quant_desc *n, const void *x, void *q, float *
  * A [M, K] with sA [M, ceil(K / 128)] (kdn_quantize with block_rows 1, or
  * kdn_rms_norm_quant), B [N, K] with sB [ceil(N / 128), ceil(K / 128)]
  * (block_rows 128), C [M, N] in dtype with rows ldc >= N elements apart (what
- * lies behind the N columns of a row is not written).  Sums are float32, rounded
- * once into C.  K a multiple of 16 (0: C is zero) up to 2^23, the other sizes up to
+ * lies behind the N columns of a row is not written).
+ * The sums of a float32 C are float32's.  For a bfloat16 C the products go, in eights,
+ * through the 8-bit matrix instruction, which aligns eight products to the largest and
+ * drops what lies 2^-14 below it before they are added in float32: beside float32's
+ * own roundings
+ *   |error of C| <= 7 2^-14 sum_k |A B| + 2^-8 |C|   (the sum with its scales),
+ * on operands of random signs far below C's own rounding, but not where large products
+ * cancel: take a float32 C there.  (Where there are few rows, whose product is bound by
+ * memory, the sums of a bfloat16 C are float32's too.)  K a multiple of 16 (0: C is zero) up to 2^23, the other sizes up to
  * 2^26, and fewer than 2^22 tiles of 64 x 64 of C (KDN_ERR_UNSUPPORTED otherwise).  A, B and C
  * 16-byte aligned; C must not alias an input. */
 typedef struct {
