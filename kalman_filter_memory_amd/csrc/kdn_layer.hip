@@ -536,16 +536,18 @@ kdn_status layer_quant_t(const kdn_layer_desc* d, const kdn_norm_desc& n, const 
     void *a = at(ws, w.a), *nu = at(ws, w.nu), *r = at(ws, w.r);
     kdn_status e = kdn_rms_norm_quant(&n, x, residual, norm_weight, x8, scale, s, nullptr, st);
     if (e != KDN_OK) return e;
-    const kdn_gemm_desc in = gemm_desc(M, n_in(d), D, w.ldz, d->dtype);
-    e = kdn_quant_gemm(&in, x8, scale, W_in, W_in_scale, Z, st);
-    if (e != KDN_OK) return e;
-    if (launch_in<E>(d->d_k, dv, Z, w.ldz, b_gate, M, H, d->T, q, k, v, a, nu, r, st) != hipSuccess)
-        return KDN_ERR_HIP;
-    const kdn_desc c = core_desc(d);
-    e = kdn_forward(&c, q, k, v, a, nu, r, lambda0, S0, o, S_T, lambda_T, at(ws, w.core),
-                    w.total - w.core, st);
-    if (e != KDN_OK) return e;
-    if (launch_out_quant<E>(dv, o, x8, scale, M, H, d->T, st) != hipSuccess) return KDN_ERR_HIP;
+    if (H > 0) {
+        const kdn_gemm_desc in = gemm_desc(M, n_in(d), D, w.ldz, d->dtype);
+        e = kdn_quant_gemm(&in, x8, scale, W_in, W_in_scale, Z, st);
+        if (e != KDN_OK) return e;
+        if (launch_in<E>(d->d_k, dv, Z, w.ldz, b_gate, M, H, d->T, q, k, v, a, nu, r, st) != hipSuccess)
+            return KDN_ERR_HIP;
+        const kdn_desc c = core_desc(d);
+        e = kdn_forward(&c, q, k, v, a, nu, r, lambda0, S0, o, S_T, lambda_T, at(ws, w.core),
+                        w.total - w.core, st);
+        if (e != KDN_OK) return e;
+        if (launch_out_quant<E>(dv, o, x8, scale, M, H, d->T, st) != hipSuccess) return KDN_ERR_HIP;
+    }  // (no heads: s is still x + residual, and y a product of depth 0: zeros)
     const kdn_gemm_desc out = gemm_desc(M, D, H * dv, D, d->dtype);
     return kdn_quant_gemm(&out, x8, scale, W_out, W_out_scale, y, st);
 }
@@ -632,7 +634,7 @@ kdn_status kdn_layer_quant_forward(const kdn_layer_desc* d, const void* x, const
                                    void* stream) {
     const kdn_status st = check_quant_layer(d, residual_dtype, eps);
     if (st != KDN_OK) return st;
-    if (d->B == 0 || d->H == 0) return KDN_OK;
+    if (d->B == 0 || (d->H == 0 && d->T == 0)) return KDN_OK;
     if (!ws) return KDN_ERR_NULL;
     const QuantLayerWs w = quant_layer_ws(d);
     if (d->T == 0) {  // no token rows: only the state passes through
@@ -641,8 +643,8 @@ kdn_status kdn_layer_quant_forward(const kdn_layer_desc* d, const void* x, const
         return kdn_forward(&c, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, lambda0, S0,
                            nullptr, S_T, lambda_T, at(ws, w.core), w.total - w.core, stream);
     }
-    if (!x || !norm_weight || !W_in || !W_in_scale || !b_gate || !W_out || !W_out_scale || !y)
-        return KDN_ERR_NULL;
+    if (!x || !norm_weight || !y) return KDN_ERR_NULL;
+    if (d->H > 0 && (!W_in || !W_in_scale || !b_gate || !W_out || !W_out_scale)) return KDN_ERR_NULL;
     if ((residual != nullptr) != (s != nullptr)) return KDN_ERR_NULL;
     if (ws_bytes < w.total) return KDN_ERR_WORKSPACE;
     for (const void* p : {x, residual, (const void*)norm_weight, W_in, W_out, (const void*)y,
