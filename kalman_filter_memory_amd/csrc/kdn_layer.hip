@@ -622,7 +622,8 @@ kdn_status kdn_layer_forward(const kdn_layer_desc* d, void* blas, const void* x,
 
 size_t kdn_layer_quant_workspace_bytes(const kdn_layer_desc* d) {
     if (check_quant_layer(d, KDN_F32, 0.f) != KDN_OK) return 0;
-    return quant_layer_ws(d).total;
+    // (an empty batch needs none, but 0 says that the descriptor is invalid)
+    return std::max<size_t>(quant_layer_ws(d).total, 16);
 }
 
 kdn_status kdn_layer_quant_forward(const kdn_layer_desc* d, const void* x, const void* residual,

@@ -53,3 +53,24 @@ def test_without_heads(B, T, D, dtype, res, variant):
         assert y.dtype == dtype and int((y != 0).sum()) == 0 and not torch.isnan(y.float()).any()
         assert torch.equal(s, want)
         assert S_T.shape == (B, 0, 32, 32) and lam.numel() == 0
+
+
+@pytest.mark.parametrize("B,T,H", [(0, 5, 2), (0, 0, 2), (2, 0, 0), (0, 0, 0)])
+def test_empty_sizes_are_valid_descriptors(B, T, H):
+    """0 bytes of workspace are the answer for an invalid descriptor alone."""
+    d = kdn.make_layer_desc(B, T, H, 64, 32, 32, 16, "diagonal", kdn.F32)
+    assert kdn.layer_quant_workspace_bytes(d) > 0
+    args = _args(**{n: None for n in ("x", "residual", "nw", "y", "s", "ws")}, n=0)
+    assert kdn.load_library().kdn_layer_quant_forward(ctypes.byref(d), *args) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,H", [(0, 5, 2), (0, 0, 2), (2, 0, 0), (2, 0, 2), (0, 3, 0)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_empty_batches(B, T, H, residual):
+    D = 64
+    x = torch.empty(B, T, D).cuda()
+    S0 = torch.randn(B, H, 32, 32).cuda()
+    y, s, S_T, lam = kdn.layer_quant_forward(x, torch.ones(D).cuda(), *_weights(H, D), H, 32, 32,
+                                             residual=x.clone() if residual else None, S0=S0, chunk=16)
+    assert y.shape == s.shape == x.shape and torch.equal(S_T, S0) and lam.shape == (B, H, 32)
