@@ -266,6 +266,12 @@ hipError_t launch_out_quant(int dv, const void* o, void* q, float* scale, int M,
     return hipErrorInvalidValue;
 }
 
+// y of a layer without heads (a kernel and no memset: the call may be captured)
+__global__ __launch_bounds__(256) void zero_kernel(kdn::u32x4* y, size_t n16) {
+    for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n16; i += size_t(gridDim.x) * 256)
+        y[i] = kdn::u32x4{0, 0, 0, 0};
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct LayerWs {
@@ -589,9 +595,18 @@ kdn_status kdn_layer_forward_events(const kdn_layer_desc* d, void* blas, const v
     kdn_status st = check_layer(d);
     if (st != KDN_OK) return st;
     if (size_t(d->B) * d->T == 0 || d->H == 0) {
-        // no token rows: only the state passes through (the core call does that)
+        // no heads, or no token rows: only the state passes through (the core call does that)
         const kdn_desc c = core_desc(d);
-        if (d->B * d->H == 0) return KDN_OK;
+        const size_t rows = size_t(d->B) * d->T;
+        if (rows > 0) {  // no heads: y is a product of depth 0
+            if (!y) return KDN_ERR_NULL;
+            if (!aligned16(y)) return KDN_ERR_ALIGN;
+            const size_t n16 = rows * d->d_model * (d->dtype == KDN_BF16 ? 2 : 4) / 16;
+            zero_kernel<<<unsigned(std::min<size_t>((n16 + 255) / 256, 4096)), 256, 0,
+                          static_cast<hipStream_t>(stream)>>>(static_cast<kdn::u32x4*>(y), n16);
+            return hipGetLastError() == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+        }
+        if (d->B == 0 || d->H == 0) return KDN_OK;
         const LayerWs w = layer_ws(d);
         if (!ws) return KDN_ERR_NULL;
         if (ws_bytes < w.total) return KDN_ERR_WORKSPACE;
