@@ -527,7 +527,9 @@ kdn_status kdn_layer_quant_forward(const kdn_layer_desc *d, const void *x, const
  * B*H up to 2^24 - 1, and at most 2^24 - 1 workgroups (KDN_ERR_UNSUPPORTED
  * otherwise).  State and sums are float32.  Every pointer 16-byte aligned.
  * |a| <= 1 is expected (not checked): products of a over a run of tokens are
- * formed, and must stay in float32's range.  a_t = 0 starts anew at token t. */
+ * formed, and must stay in float32's range.  a_t = 0 starts anew at token t.  How the
+ * tokens are bracketed depends on T, d and the types alone: a sequence gives the same
+ * bits alone and in any batch. */
 typedef struct {
     int32_t B, H, T, d;
     int32_t dtype;      /* kdn_dtype */

@@ -22,8 +22,9 @@
 // as it has it, and 16 tiles form a group: a tile folds the maps of its group
 // before it, in order, and applies them to the state at the group's start, which
 // the last tile of the group before publishes; so the chain is T / (16 tile)
-// steps long.  The bracketing is fixed by T alone, so the same inputs give the same
-// bits.  A workgroup takes its tile from a counter, in an order in which a tile
+// steps long.  The walk folds its tiles in the same groups, so the bracketing is fixed by
+// T, d and the types: a sequence gives the same bits alone and in any batch.  A workgroup
+// takes its tile from a counter, in an order in which a tile
 // comes after everything it waits for: whoever holds an earlier tile is already
 // running and waits for earlier tiles only, so every wait ends.
 // The rule: the walk where it has two tiles at most, where the pairs are 1024 or more, four
@@ -177,12 +178,15 @@ __global__ __launch_bounds__(kThreads) void gated_kernel(ScanArgs p) {
     const int ng = (p.nt + kGroup - 1) / kGroup;
     // the thread that carries channel c0 + tid between tiles
     const bool carrier = tid < CB && c0 + tid < p.d;
-    float state = 0.f;
+    float state = 0.f;  // enters the tile
+    // walk: the state at the start of its group of tiles, and the map of the group so far
+    float start = 0.f, gA = 1.f, gX = 0.f;
     if (carrier && j0 == 0) {
-        if (p.first != nullptr) state = p.first[seq * p.d + c0 + tid];
+        if (p.first != nullptr) start = p.first[seq * p.d + c0 + tid];
+        state = start;
         // read by tile 0 alone and passed on from there, so that the state that
         // leaves may be written over it
-        if constexpr (CHAIN) publish(p.chain.start + seq * ng * p.d + c0 + tid, state);
+        if constexpr (CHAIN) publish(p.chain.start + seq * ng * p.d + c0 + tid, start);
     }
 
     for (int j = j0; j < j1; ++j) {
@@ -257,9 +261,18 @@ __global__ __launch_bounds__(kThreads) void gated_kernel(ScanArgs p) {
                     if (j % kGroup == kGroup - 1 && j + 1 < p.nt)
                         publish(p.chain.start + (seq * ng + j / kGroup + 1) * p.d + ch,
                                 fmaf(PA, state, PX));
+                } else {
+                    // as chain_wait folds them
+                    state = j % kGroup == 0 ? start : fmaf(gA, start, gX);
+                    gX = fmaf(PA, gX, PX);
+                    gA *= PA;
+                    if (j % kGroup == kGroup - 1) {
+                        start = fmaf(PA, state, PX);
+                        gA = 1.f;
+                        gX = 0.f;
+                    }
                 }
                 hin[tid] = state;
-                state = fmaf(PA, state, PX);
             }
         }
         __syncthreads();
