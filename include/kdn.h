@@ -527,9 +527,13 @@ kdn_status kdn_layer_quant_forward(const kdn_layer_desc *d, const void *x, const
  * B*H up to 2^24 - 1, and at most 2^24 - 1 workgroups (KDN_ERR_UNSUPPORTED
  * otherwise).  State and sums are float32.  Every pointer 16-byte aligned.
  * |a| <= 1 is expected (not checked): products of a over a run of tokens are
- * formed, and must stay in float32's range.  a_t = 0 starts anew at token t.  How the
- * tokens are bracketed depends on T, d and the types alone: a sequence gives the same
- * bits alone and in any batch. */
+ * formed, and the sums of a run that starts from zero, and both must stay in float32's
+ * range (a product that falls below it is 0).  a_t = 0 starts anew at token t.  An
+ * infinity or NaN in x or in a state makes its channel's states from its token on (the
+ * backward: its gradients up to its token) infinite or NaN - NaN also where the gates
+ * alone would have kept an infinity, whose product with a run's 0 it is - and nothing
+ * else.  How the tokens are bracketed depends on T, d and the types alone: a sequence
+ * gives the same bits alone and in any batch. */
 typedef struct {
     int32_t B, H, T, d;
     int32_t dtype;      /* kdn_dtype */

@@ -903,6 +903,8 @@ def make_scan_desc(B, H, T, d, dtype, gate_dtype) -> KdnScanDesc:
 def gated_scan(x, a, h0=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + x_t per channel: x, a
     [B,H,T,d] (float32 or bfloat16 each), h0 float32 [B,H,d] or None (zeros).
+    |a| <= 1 is expected.  An infinity or NaN makes its channel infinite or NaN from its
+    token on (not always the infinity that the recurrence would keep).
     Returns (h in x's dtype [B,H,T,d], h_T float32 [B,H,d])."""
     dev = _tensors(("x", x), ("a", a), ("h0", h0))
     if x.dim() != 4 or a.shape != x.shape:
