@@ -436,7 +436,8 @@ kdn_status kdn_rms_norm(const kdn_norm_desc *n, const void *x, const void *resid
                         const float *weight, void *y, void *s, float *rstd, void *stream);
 
 /* The same with y in 8 bits (from float32, not by way of dtype): q [rows, d]
- * e4m3 and scale [rows, ceil(d / 128)] float32, an operand of kdn_quant_gemm. */
+ * e4m3 and scale [rows, ceil(d / 128)] float32, an operand of kdn_quant_gemm where d is
+ * a multiple of 16. */
 kdn_status kdn_rms_norm_quant(const kdn_norm_desc *n, const void *x, const void *residual,
                               const float *weight, void *q, float *scale, void *s, float *rstd,
                               void *stream);

@@ -35,7 +35,13 @@
 // 627; 215 x 335 x 128 float32 28.4, 34.5; 16 x 200 x 128 float32 backward, two tiles, 10.1,
 // 13.6; but 406 pairs of 826 tokens in float32 123, 106, 64 x 1000 x 128 bfloat16 24.3,
 // 16.5.)  B1 H16 T65536 d128 bfloat16, a chain, runs at 5.2 TB/s in 154 us with its 5.5 us
-// of clearing; the backward of B8 H16 T4096 takes 188 us, 5.0 TB/s.
+// of clearing; the backward of B8 H16 T4096 takes 188 us, 5.0 TB/s.  16 x 16384 x 128, a
+// chain: float32 94.5 us (4.3 TB/s), x bfloat16 and a float32 67 (4.0), x float32 and a
+// bfloat16 78 (4.3); the backward 146 (4.6; as a chain 256 and 16 registers, one wave per
+// SIMD, where the walk's 240 leave two), 106 and 119 (5.1).  Few channels wait for the
+// chain: 500000 x 32 bfloat16 39 us (2.4 TB/s), 31 groups one after the other; a block of
+// channels that is not full leaves lanes idle: 9 x 6521 x 200 bfloat16, 72 of 128 channels
+// in the second block, 26 us (2.7 TB/s).
 // A published word is one atomic access whose value cannot be the mark "not yet
 // there" (all bits set), so it needs no flag and no fence.
 #include <hip/hip_runtime.h>

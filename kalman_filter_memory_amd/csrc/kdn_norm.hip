@@ -47,8 +47,12 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x, float* red)
 // 16 neighbouring threads hold one block of 128 columns, so its maximum is four
 // DPP steps.  A wave per row, up to 1024 columns, meets no barrier; wider rows
 // would leave too few waves to hide the loads.
-// 32768 x 2048 bfloat16 with residual to 8 bits: 82 us, 5.8 TB/s (above what a copy
-// reaches, which writes more of its bytes); 256 rows of it 4.2 us, 1537 x 2056 float32 10.8 us (4.7 TB/s).
+// 32768 x 2048 bfloat16 with residual to 8 bits: 83 us, 5.7 TB/s (above what a copy
+// reaches, which writes more of its bytes); 1537 x 2056 float32 10.2 us (5.0 TB/s).  Bound
+// by latency where there are few rows (256 of them: 3.1 us, a launch and the loads of x, of
+// the residual and, behind the sum, of w, one after the other), and by lanes without a
+// column where they are narrow (500000 x 64 without residual to 8 bits: 129 us, 0.8 TB/s,
+// 8 of 64 lanes at work; 500000 x 128 129 us).
 template <typename Ex, typename Er, bool RES, bool QUANT, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
     int rows, int d, float eps, const Ex* __restrict__ x, const Er* residual,
@@ -122,7 +126,10 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(
 // of them and the workgroup writes one partial row of dw, which dw_kernel adds
 // up in a fixed order (no atomics: the same inputs give the same bits).  1024
 // workgroups leave 8 MB of partial rows at 2048 columns.
-// 32768 x 2048 bfloat16: 147 us and 6 us for dw, 5.3 TB/s.
+// 32768 x 2048 bfloat16: 152 us, 5 of them for dw, 5.3 TB/s.  Up to 4096 columns four waves
+// or more share a SIMD; up to 8192 two (174 registers; 8192 x 8192 180 us, 4.5 TB/s), beyond
+// that xh, dn and dw leave room for one, and the loads' latency shows (256 and 62 registers;
+// 4096 x 16384 287 us, 2.8 TB/s).  500000 x 64, 8 of 64 lanes at work: 260 us, 1.5 TB/s.
 template <typename Ex, typename Er, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(
     int rows, int d, const Ex* __restrict__ dy, const Er* __restrict__ s,
@@ -312,8 +319,8 @@ kdn_status check_norm(const kdn_norm_desc* n) {
 }
 
 // Threads per row: a wave, while the row fits a wave's registers; more for wide rows.
-// (the rule by both sides, to 8 bits and backward: 32768 x 2048 93 and 168 us with a wave,
-// 82 and 158 with four; 32768 x 1024 37 and 68 against 42 and 80)
+// (the rule by both sides, bfloat16, to 8 bits and backward: 32768 x 2048 94 and 163 us with
+// a wave, 83 and 152 with four; 32768 x 1024 37 and 80 against 42 and 97)
 bool wave_rows(int d) { return d <= 1024; }
 
 struct NormArgs {
@@ -382,7 +389,8 @@ kdn_status norm_call(const kdn_norm_desc* n, const void* x, const void* residual
 
 // workgroups of the backward: enough to fill the GPU, few enough that their
 // partial dw rows stay small beside the rows themselves (us, bfloat16, 512 and 1024: 1000 x
-// 8192 22.7, 28.6; 2048 x 8192 31, 37; 4096 x 4096 28.0, 27.6; 16384 x 2048 45, 40)
+// 8192 25.3, 31.5; 2048 x 8192 39.5, 44.6; 4096 x 4096 36.8, 38.2; 16384 x 2048 97, 81;
+// 32768 x 2048 186, 151)
 int bwd_groups(const kdn_norm_desc* n) {
     const int rpb = wave_rows(n->d) ? 4 : 1;
     const int64_t units = (n->rows + rpb - 1) / rpb;

@@ -141,8 +141,10 @@ template <int N> __device__ __forceinline__ void step_wait() {
 // by then everybody has read the step's operands, whose buffer is filled anew, and
 // has its part of the next step's, whose first fragments are read while those
 // products run.
-// Measured (bfloat16 results): 8192^3 425 us, 2.6 PFLOP/s; 32768 x 6192 x 2048 406 us, 2.05
-// PFLOP/s, the matrix unit busy 51 % of its cycles at 2.0 GHz.  Timing copies without
+// Measured (bfloat16 results): 8192^3 429 us, 2.6 PFLOP/s; 32768 x 6192 x 2048 408 to 424 us,
+// 2.0 PFLOP/s, the matrix unit busy 51 % of its cycles at 2.0 GHz: a step takes 1.56 us, and
+// a tile 6 us besides, its first loads and its C, with nothing beside them, since one
+// workgroup fills a CU.  Float32 results: 760 and 881 us.  Timing copies without
 // the copies into LDS, or without the fragments' reads, take 379 and 298 us where the
 // whole took 490 (8192^3): both ways through LDS bound it, and the multiply-adds.
 //
@@ -167,8 +169,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
     const int wm = wave % WM, wn = wave / WM;
     // each XCD (workgroups are handed to the eight in turn) takes a run of tiles, and
     // walks it in strips of 6 tiles of m, so that its 32 CUs work on about 6 x 5 tiles at
-    // a time and read the least through its L2 (32768 x 6192 x 2048: 406 us, in strips of
-    // 4 408, of 8 435, of 16 478)
+    // a time and read the least through its L2 (us in strips of 4, 6, 8, 16 tiles: 32768 x
+    // 6192 x 2048 425, 410, 430, 473; 8192^3 430, 433, 430, 441; 16384 x 4096 x 4096 228,
+    // 229, 228, 236; 4096 x 16384 x 2048 131, 130, 131, 132; 32768 x 2048 x 2048 131, 131,
+    // 132, 132)
     constexpr int STRIP = 6;
     const int total = p.mt * p.nt;
     int t = blockIdx.x;
@@ -448,8 +452,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 2) void qgemm_kernel(GemmArgs p)
 // workgroup has to have its share of them in flight at once.  A workgroup takes 16
 // columns and all of K, its W waves the blocks w, w + W, ...; fragments go from
 // memory straight into registers, and the waves' sums meet in LDS in their order.
-// 1 x 6192 x 2048: 4.1 us (3.1 TB/s); 1 x 8192 x 8192: 12.8 us (5.2 TB/s); 16 x 2048 x 2048:
-// 4.0 us.
+// 1 x 6192 x 2048: 4.4 us (2.9 TB/s); 1 x 8192 x 8192: 12.6 us (5.3 TB/s); 16 x 2048 x 2048:
+// 4.4 us.  A wave waits for the loads of each of its blocks, two of them one after the
+// other at K 2048: latency bounds the short ones, memory the long ones.
 template <int TM, int W, typename Eo>
 __global__ __launch_bounds__(64 * W) void qgemm_few_kernel(GemmArgs p) {
     using Op = Block<true>;
@@ -528,12 +533,12 @@ template <int BM, int BN, int WM, int WN, int S, int KS, typename Eo> void launc
 
 template <typename Eo> void launch_gemm(const GemmArgs& a, hipStream_t st) {
     const unsigned cols = unsigned((a.N + 15) / 16);
-    // Few rows, and no more than one workgroup per CU: 16 x 2048 x 2048 takes 4.0 us against
-    // 4.9 in tiles of 32 x 32, 12 x 4096 x 4096 6.0 against 6.4, but 16 x 6192 x 2048 6.3
-    // against 4.9 and 16 x 8192 x 8192 19.5 against 15.2, for every
-    // workgroup reads every row of A.  Up to four rows are ahead anywhere (4 x 8192 x 8192 13.9 against 15.0, 1 row
-    // 12.8 against 14.9), 17 to 32 with a short K (24 x 1000 x 1024 3.5 against 4.2; 32 x
-    // 2048 x 2048 5.5 against 4.9).
+    // Few rows, and no more than one workgroup per CU (bfloat16): 16 x 2048 x 2048 takes 4.4
+    // us against 5.3 in tiles of 32 x 32, 16 x 4096 x 8192 11.5 against 13.0, but 16 x 6192 x
+    // 2048 6.6 against 5.3 and 16 x 8192 x 8192 20.5 against 15.5, for every workgroup reads
+    // every row of A.  Up to four rows are ahead anywhere (4 x 8192 x 8192 14.8 against 15.4,
+    // 1 row 12.8 against 15.8), 17 to 32 with a short K (24 x 1000 x 1024 3.7 against 4.4; 32
+    // x 2048 x 2048 5.7 against 5.1).
     if (a.M <= 4 || (a.M <= 16 && cols <= 256)) {
         qgemm_few_kernel<1, 8, Eo><<<cols, 512, 0, st>>>(a);
     } else if (a.M <= 32 && cols <= 256 && a.kb <= 8) {
