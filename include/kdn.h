@@ -562,8 +562,8 @@ kdn_status kdn_gated_scan_backward(const kdn_scan_desc *s, const void *a, const 
                                    float *da, float *dh0, void *ws, size_t ws_bytes, void *stream);
 
 /* One token in place: x, a, o [B,H,d]; h [B,H,d] float32 is read and
- * overwritten, and o is its new value in dtype.  s->T is ignored but must not be
- * negative.  slot NULL, or device int32 [B]: h is then a cache
+ * overwritten, and o is its new value in dtype.  s->T is not used, but held to the
+ * descriptor's limits.  slot NULL, or device int32 [B]: h is then a cache
  * [n_slots,H,d] and sequence b's state is at slot[b]; outside [0, n_slots) the
  * sequence is idle (its state and its o row are not touched).  Slots of active
  * sequences must be distinct (not checked). */

@@ -772,7 +772,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, in_place=False):
 
 
 def rms_norm_quant(x, weight, residual=None, eps=1e-6, in_place=False):
-    """rms_norm with y in 8 bits, an operand of quant_matmul.  Returns (q
+    """rms_norm with y in 8 bits, an operand of quant_matmul where d is a multiple of
+    16 (as its depth has to be).  Returns (q
     float8_e4m3fn [..., d], scale float32 [..., ceil(d / 128)], s)."""
     dev = _tensors(("x", x), ("weight", weight), ("residual", residual))
     n = _norm_desc(x, "x", weight, x.dtype if residual is None else residual.dtype, eps)
