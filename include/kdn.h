@@ -570,6 +570,62 @@ kdn_status kdn_gated_scan_backward(const kdn_scan_desc *s, const void *a, const 
 kdn_status kdn_gated_scan_step(const kdn_scan_desc *s, const void *x, const void *a, float *h,
                                const int32_t *slot, int32_t n_slots, void *o, void *stream);
 
+/* ------------------------------------------------------- gated delta rule
+ * The layer with the gain in place of its uncertainty: the special case of the
+ * recurrence whose predictive covariance is a per-token isotropic stand-in and is
+ * not tracked ("Kalman Delta Networks", English abstract and summary: the Delta
+ * rule as a special case), with the decay given as its logarithm:
+ *   S_t = e^g_t S_{t-1} + beta_t (v_t - e^g_t S_{t-1} k_t) k_t^T
+ *   o_t = scale S_t q_t
+ * q, k [B,Hk,T,d_k]; v, o [B,H,T,d_v]; g, beta [B,H,T]; S [B,H,d_v,d_k] float32.
+ * Head h of the values reads head h / (H / Hk) of the queries and keys (H a
+ * multiple of Hk).  d_k, d_v in {32, 64, 128}; B*H below 2^20; T up to 2^30
+ * (KDN_ERR_UNSUPPORTED otherwise).  dtype: q, k, v, o; gate_dtype: g and beta.
+ *
+ * Packed: cu_seqlens (device int32 [B+1], non-decreasing, from 0 to T) not NULL
+ * lays B sequences end to end along T: q, k [Hk,T,d_k]; v, o [H,T,d_v]; g, beta
+ * [H,T]; a state per sequence and head as above.  Offsets outside [0, T] or
+ * decreasing are clamped (no memory outside the buffers is touched, but the
+ * results are not those of the sequences meant); rows in no sequence are not
+ * written.  NULL: B sequences of T tokens.
+ *
+ * Expected, not checked: g <= 0 (a decay below 2^-160 counts as 0: an infinitely
+ * negative g forgets a finite state), and keys and beta for which the
+ * recurrence itself does not grow (|k| <= 1 and beta <= 2).  The tokens of a block of 32 are solved together:
+ * an infinity or NaN in a token makes outputs of its own block and of later tokens
+ * of its head non-finite (a value's: its column alone), and nothing of other
+ * sequences and heads.
+ * Sums and states have float32's accuracy for both types (kernels: products of
+ * operands split into bfloat16 parts that together hold all of a float32's bits). */
+typedef struct {
+    int32_t B, H, Hk, T, d_k, d_v;
+    int32_t dtype;      /* kdn_dtype */
+    int32_t gate_dtype; /* kdn_dtype */
+    float scale;
+} kdn_delta_desc;
+
+/* Bytes of workspace kdn_gated_delta needs (0 if the descriptor is invalid; 16:
+ * none, ws may be NULL).  Host-only. */
+size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc *d);
+
+/* The recurrence over all tokens from S0 (NULL: zeros).  S_T: NULL or the last
+ * states (S0 for a sequence without tokens), may be S0's buffer; o must not alias
+ * an input.  q, k, v, o, S0, S_T and ws 16-byte aligned. */
+kdn_status kdn_gated_delta(const kdn_delta_desc *d, const int32_t *cu_seqlens, const void *q,
+                           const void *k, const void *v, const void *g, const void *beta,
+                           const float *S0, void *o, float *S_T, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* One token in place: q, k [B,Hk,d_k]; v, o [B,H,d_v]; g, beta [B,H]; S
+ * [B,H,d_v,d_k] is read and overwritten.  d->T is not used.  slot NULL, or device
+ * int32 [B]: S is then a cache [n_slots,H,d_v,d_k] and sequence b's state is at
+ * slot[b]; outside [0, n_slots) the sequence is idle (its state and its o row are
+ * not touched).  Slots of active sequences must be distinct (not checked).  q, k
+ * and S 16-byte aligned. */
+kdn_status kdn_gated_delta_step(const kdn_delta_desc *d, const void *q, const void *k,
+                                const void *v, const void *g, const void *beta, float *S,
+                                const int32_t *slot, int32_t n_slots, void *o, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,9 @@ Functions (same names as the C entry points):
                       residual=None, ...) -> (y, s, S_T, lambda_T)   (the layer in 8 bits)
   gated_scan(x, a, h0=None) -> (h, h_T);  gated_scan_step(x, a, h, slot=None) -> o
   gated_scan_backward(a, h, dh, h0=None, dh_T=None) -> dict of float32 gradients (dx, da, dh0)
+  gated_delta(q, k, v, g, beta, S0=None) -> (o, S_T)      (the gated delta rule)
+  gated_delta_varlen(q, k, v, g, beta, cu_seqlens, S0=None) -> (o, S_T)   (a packed batch)
+  gated_delta_step(q, k, v, g, beta, S, slot=None) -> o   (one token, S in place)
 """
 from __future__ import annotations
 
@@ -60,6 +63,7 @@ EXPORTS = (
     "kdn_layer_quant_workspace_bytes", "kdn_layer_quant_forward",
     "kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes",
     "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
+    "kdn_gated_delta_workspace_bytes", "kdn_gated_delta", "kdn_gated_delta_step",
 )
 
 
@@ -90,6 +94,11 @@ class KdnGemmDesc(ctypes.Structure):
 
 class KdnScanDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "T", "d", "dtype", "gate_dtype")]
+
+
+class KdnDeltaDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "Hk", "T", "d_k", "d_v", "dtype",
+                                               "gate_dtype")] + [("scale", ctypes.c_float)])
 
 
 class KdnError(RuntimeError):
@@ -172,6 +181,11 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_gated_scan.argtypes = [G] + [P] * 6 + [S, P]
     lib.kdn_gated_scan_backward.argtypes = [G] + [P] * 9 + [S, P]
     lib.kdn_gated_scan_step.argtypes = [G] + [P] * 4 + [ctypes.c_int32, P, P]
+    E = ctypes.POINTER(KdnDeltaDesc)
+    lib.kdn_gated_delta_workspace_bytes.argtypes = [E]
+    lib.kdn_gated_delta_workspace_bytes.restype = S
+    lib.kdn_gated_delta.argtypes = [E] + [P] * 10 + [S, P]
+    lib.kdn_gated_delta_step.argtypes = [E] + [P] * 7 + [ctypes.c_int32, P, P]
     _lib = lib
     return lib
 
@@ -964,4 +978,102 @@ def gated_scan_step(x, a, h, slot=None, out=None):
     o = out if out is not None else torch.empty_like(x)
     _launch("kdn_gated_scan_step", dev, ctypes.byref(s), x.data_ptr(), a.data_ptr(), h.data_ptr(),
             _ptr(slot), n_slots, o.data_ptr())
+    return o
+
+
+def make_delta_desc(B, H, Hk, T, d_k, d_v, dtype, gate_dtype, scale=None) -> KdnDeltaDesc:
+    return KdnDeltaDesc(*_int32(B, H, Hk, T, d_k, d_v), dtype, gate_dtype,
+                        d_k ** -0.5 if scale is None and d_k else float(scale or 0.0))
+
+
+def _delta_desc(q, k, v, g, beta, scale, cu_seqlens=None, one_token=False):
+    """(descriptor, states) after checks of the inputs' shapes and types; lead: B, H and
+    T of the values, or what stands for them."""
+    lead, name = ((3, "[B,H,T,d]") if not one_token and cu_seqlens is None else
+                  (2, "[H,T,d]" if cu_seqlens is not None else "[B,H,d]"))
+    if q.dim() != lead + 1 or v.dim() != lead + 1:
+        raise ValueError(f"q, k and v must be {name}")
+    if q.dtype != v.dtype:
+        raise TypeError("q, k, v must share one dtype")
+    _shaped("k", k, q.dtype, q.shape)
+    _shaped("g", g, g.dtype, v.shape[:-1])
+    _shaped("beta", beta, g.dtype, v.shape[:-1])
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must be int32 [N+1]")
+        B, (Hk, T), (H, Tv) = cu_seqlens.shape[0] - 1, q.shape[:2], v.shape[:2]
+        same = T == Tv
+    else:
+        B, Hk, H = q.shape[0], q.shape[1], v.shape[1]
+        T = 1 if one_token else q.shape[2]
+        same = v.shape[0] == B and (one_token or v.shape[2] == T)
+    if not same or (H % Hk if Hk else H):
+        raise ValueError("q, k and v must agree in all but heads and width, the heads of v "
+                         "a multiple of those of q and k")
+    return make_delta_desc(B, H, Hk, T, q.shape[-1], v.shape[-1], _dtype_code(q.dtype),
+                           _dtype_code(g.dtype), scale)
+
+
+def _gated_delta(q, k, v, g, beta, cu_seqlens, S0, scale, out):
+    dev = _tensors(("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta),
+                   ("cu_seqlens", cu_seqlens), ("S0", S0))
+    d = _delta_desc(q, k, v, g, beta, scale, cu_seqlens)
+    states = (d.B, d.H, d.d_v, d.d_k)
+    _shaped("S0", S0, torch.float32, states)
+    if out is None:
+        o, S_T = torch.empty_like(v), _empty(states, torch.float32, dev)
+    else:
+        o, S_T = out
+        _tensors(("q", q), ("o", o), ("S_T", S_T))
+        _shaped("o", o, v.dtype, v.shape)
+        _shaped("S_T", S_T, torch.float32, states)
+    need = load_library().kdn_gated_delta_workspace_bytes(ctypes.byref(d))
+    ws = _empty((need,), torch.uint8, dev) if need > 16 else None
+    _launch("kdn_gated_delta", dev, ctypes.byref(d), _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0), o.data_ptr(), _ptr(S_T),
+            _ptr(ws), need)
+    return o, S_T
+
+
+def gated_delta(q, k, v, g, beta, S0=None, scale=None, out=None):
+    """Gated delta rule S_t = e^g_t S_{t-1} + beta_t (v_t - e^g_t S_{t-1} k_t) k_t^T,
+    o_t = scale S_t q_t.  q, k [B,Hk,T,d_k] and v [B,H,T,d_v] float32 or bfloat16, H a
+    multiple of Hk (head h of v reads head h / (H / Hk) of q and k); g (the decay's
+    logarithm, <= 0; -inf forgets) and beta [B,H,T] float32 or bfloat16; S0 float32
+    [B,H,d_v,d_k] or None (zeros); scale: d_k ** -0.5 unless given.  Keys are expected
+    normalised (|k| <= 1, beta <= 2).  Returns (o in v's dtype [B,H,T,d_v], S_T float32
+    [B,H,d_v,d_k]).  out: optional preallocated (o, S_T); S_T may be S0."""
+    return _gated_delta(q, k, v, g, beta, None, S0, scale, out)
+
+
+def gated_delta_varlen(q, k, v, g, beta, cu_seqlens, S0=None, scale=None, out=None):
+    """gated_delta of a packed batch: q, k [Hk,T,d_k]; v [H,T,d_v]; g, beta [H,T] with N
+    sequences laid end to end along T (cu_seqlens: int32 [N+1] on the GPU, from 0 to T);
+    S0 [N,H,d_v,d_k].  Returns (o [H,T,d_v], S_T [N,H,d_v,d_k]); rows of o in no sequence
+    are left as they were in `out`, or uninitialised."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens must be int32 [N+1]")
+    return _gated_delta(q, k, v, g, beta, cu_seqlens, S0, scale, out)
+
+
+def gated_delta_step(q, k, v, g, beta, S, slot=None, scale=None, out=None):
+    """One token of gated_delta in place: q, k [B,Hk,d_k]; v [B,H,d_v]; g, beta [B,H]; S
+    float32 [B,H,d_v,d_k] is overwritten with the new state.  slot: int32 [B] on the GPU;
+    S is then a cache [n_slots,H,d_v,d_k] and sequence b's state is at slot[b] (outside
+    [0, n_slots): idle; slots of active sequences must be distinct).  Returns o [B,H,d_v]
+    in v's dtype (rows of idle sequences are left as they were in `out`, or
+    uninitialised)."""
+    dev = _tensors(("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("S", S),
+                   ("slot", slot), ("out", out))
+    d = _delta_desc(q, k, v, g, beta, scale, one_token=True)
+    if S.dim() != 4:
+        raise ValueError("S must be [B,H,d_v,d_k], or [n_slots,H,d_v,d_k] with slot")
+    n_slots = S.shape[0]
+    _shaped("S", S, torch.float32, (d.B if slot is None else n_slots, d.H, d.d_v, d.d_k))
+    _shaped("slot", slot, torch.int32, (d.B,))
+    _shaped("out", out, v.dtype, v.shape)
+    o = out if out is not None else torch.empty_like(v)
+    _launch("kdn_gated_delta_step", dev, ctypes.byref(d), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(), _ptr(slot), n_slots,
+            o.data_ptr())
     return o

@@ -1,0 +1,474 @@
+// kdn_delta.h -- what the gated delta rule's kernels share (gfx950 only): float32
+// values as sums of bfloat16 planes, LDS tiles of token rows, and the helper waves that
+// load a chunk and prepare the two 32 x 32 matrices every head of it needs.
+//
+// Chunks are 32 tokens.  With G_t the sum of the log decays up to token t of the chunk,
+// gamma_t = e^G_t and Gamma_ts = e^(G_t - G_s), the corrections e_t = v_t - S k_t that
+// the tokens of a chunk make (S decayed, and already corrected by the tokens before)
+// solve a triangular system,
+//   (I + L diag(beta)) E = V - gamma K S_0,   L_ts = Gamma_ts k_t.k_s  (s < t),
+// and U = diag(beta) E gives the rest by plain products.
+//
+// Precision.  Matrix products run on the bfloat16 instructions (16 times the float32
+// ones' rate), with every float32 operand written as the sum of three bfloat16 planes
+// (8 bits of the mantissa each: nothing is lost) and the partial products below 2^-24
+// left out, so states, corrections and gradients of the state carry float32's accuracy.
+// bfloat16 inputs are one plane, exactly.
+#pragma once
+
+#include "../../include/kdn.h"
+#include "kdn_device.h"
+
+namespace kdn {
+namespace delta {
+
+constexpr int C = 32;  // tokens of a chunk
+
+template <int N> struct Planes {
+    bf16x8 p[N];
+};
+
+// eight floats as the sum of N planes, largest first (each the rounding of what the ones
+// before it left)
+template <int N> __device__ __forceinline__ Planes<N> split8(const float (&f)[8]) {
+    Planes<N> r;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = f[i];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            if (n + 1 < N) {
+                x[2 * i] -= __uint_as_float(w[i] << 16);
+                x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+        r.p[n] = __builtin_bit_cast(bf16x8, w);
+    }
+    return r;
+}
+
+// four floats as N planes of 8 bytes
+template <int N> __device__ __forceinline__ void split4(const float (&f)[4], uint2 (&r)[N]) {
+    float x[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t a = pack_bf16(x[0], x[1]), b = pack_bf16(x[2], x[3]);
+        r[n] = make_uint2(a, b);
+        if (n + 1 < N) {
+            x[0] -= __uint_as_float(a << 16);
+            x[1] -= __uint_as_float(a & 0xffff0000u);
+            x[2] -= __uint_as_float(b << 16);
+            x[3] -= __uint_as_float(b & 0xffff0000u);
+        }
+    }
+}
+
+template <int N> __device__ __forceinline__ void join8(const Planes<N>& a, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) {
+        const u32x4 w = __builtin_bit_cast(u32x4, a.p[n]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] += __uint_as_float(w[i] << 16);
+            f[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// c += a b, the products of planes whose orders add up to LIM at most
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ floatx4 product(const Planes<NA>& a, const Planes<NB>& b, floatx4 c) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j <= LIM) c = Mma<bf16_t>::mma(a.p[i], b.p[j], c);
+    return c;
+}
+
+// ------------------------------------------------------------------ token rows in LDS
+// Rows of D elements (a plane), the 16-byte pieces of row t stored at piece ^ f(t): both
+// the row-wise fragments (pieces of 16 rows) and the transposing reads (4 pieces of 4
+// rows) then meet every bank once at D = 128.
+template <int D> struct Rows {
+    static constexpr int kPieces = D / 8;
+    static __device__ __forceinline__ int at(int row, int piece) {
+        const int f = ((row & 3) << 2) | (((row >> 2) ^ (row >> 3)) & 3);
+        return row * D + ((piece ^ (f & (kPieces - 1))) << 3);
+    }
+    // operand rows of this lane: the row's 8 elements of `piece`
+    static __device__ __forceinline__ bf16x8 row(const bf16_t* x, int row, int piece) {
+        return *reinterpret_cast<const bf16x8*>(x + at(row, piece));
+    }
+    // operand with the tokens along the contraction: lane l gets x[t0 + 8 (l / 16) + 0..7]
+    // of column 32 j + 8 ((l % 16) / 4) + 4 h + l % 4
+    static __device__ __forceinline__ bf16x8 col(const bf16_t* x, int t0, int j, int h, int lane) {
+        const int r = t0 + 8 * (lane >> 4) + ((lane & 15) >> 2), p = 4 * j + (lane & 3);
+        const short4x lo = read_tr16(x + at(r, p) + 4 * h), hi = read_tr16(x + at(r + 4, p) + 4 * h);
+        const short8x v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8, v);
+    }
+};
+
+// A 32 x 32 operand in LDS (a plane): rows of four 16-byte pieces, piece ^ (row / 8)
+__device__ __forceinline__ int square_at(int row, int piece) {
+    return row * C + ((piece ^ ((row >> 3) & 3)) << 3);
+}
+
+// Rows of an operand whose result rows feed the next product: result tile h of a pair
+// holds at row m the index 8 (m / 4) + 4 h + m % 4, so that a lane's values of the two
+// tiles are eight consecutive ones, which is what it has to supply of the next
+// contraction.  (No exchange between lanes anywhere along the recurrence.)
+__device__ __forceinline__ int paired_row(int lane, int h) {
+    const int m = lane & 15;
+    return 8 * (m >> 2) + 4 * h + (m & 3);
+}
+
+// ------------------------------------------------------------------------- sequences
+struct Seq {
+    size_t rq, rv;  // first row of q, k and of v, o, the gates
+    int start, len;
+};
+// sequence b, head h of values: [B,H,T,..], or rows start .. start + len of [H,T,..]
+__device__ __forceinline__ Seq sequence(const int32_t* cu, int b, int h, int H, int Hk, int T) {
+    const int hk = h / (H / Hk);
+    if (cu == nullptr) return Seq{(size_t(b) * Hk + hk) * T, (size_t(b) * H + h) * T, 0, T};
+    const int s = min(max(cu[b], 0), T), e = min(max(cu[b + 1], s), T);
+    return Seq{size_t(hk) * T + s, size_t(h) * T + s, s, e - s};
+}
+
+// Sums G of the log2 decays up to each token of a chunk, as hi + lo: differences of two
+// sums are then as exact as the decays between the two tokens, also behind a strong decay
+// (float32 sums alone would leave 2^-24 |G| in every later ratio).  A decay below 2^-160
+// counts as that and leaves exactly 0 of the state (an infinitely negative g forgets,
+// without infinities in the sums); NaN stays NaN.
+struct LogSum {
+    float hi, lo;
+};
+__device__ __forceinline__ double log2_decay(float g) {
+    const double x = double(g) * 1.4426950408889634;
+    return x < -160.0 ? -160.0 : x;
+}
+// inclusive sums over the 32 lanes of each half of a wave
+__device__ __forceinline__ LogSum log_sums(float g, int lane) {
+    double x = log2_decay(g);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const double y = __shfl_up(x, d, 32);
+        x += (lane & 31) >= d ? y : 0.0;
+    }
+    const float hi = float(x);
+    return LogSum{hi, float(x - double(hi))};
+}
+// 2^(t - s)
+__device__ __forceinline__ float decay_between(LogSum t, LogSum s) { return exp2_hw((t.hi - s.hi) + (t.lo - s.lo)); }
+__device__ __forceinline__ float decay_of(LogSum t) { return exp2_hw(t.hi); }
+
+// Orders this wave's LDS writes before its own later reads (other lanes' values).
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// lane S of each row of 16, to the whole row
+template <int S> __device__ __forceinline__ float row_bcast(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x150 + S, 0xF, 0xF, true));
+}
+
+template <int S> __device__ __forceinline__ void substitute(const float (&a)[16], float (&x)[8]) {
+    if constexpr (S < 15) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(-a[S], row_bcast<S>(x[j]), x[j]);
+        substitute<S + 1>(a, x);
+    }
+}
+
+constexpr int kLdA = 36, kLdT = 20;  // floats per row: of the system, of its inverted blocks
+
+// One wave inverts I + A, A [32][kLdA] strictly lower triangular, into three planes of
+// 32 x 32 (square_at; the upper right block of `out` must hold zeros, or with REV the
+// lower left one).  Diagonal blocks of 16 by forward substitution, a row per lane and
+// half the columns in each half of the wave; the block below by two float32 products,
+// T_10 = -T_1 (A_10 T_0), the second transposed so that a lane's results are neighbours.
+// REV: A holds the transposed system with both indices reversed (which is lower
+// triangular again), and `out` gets the transposed inverse in its own order.
+template <bool REV>
+__device__ __forceinline__ void invert(const float* A, float* tmp, bf16_t* out, int lane) {
+    const int r = lane & 15, b = (lane >> 4) & 1, h = lane >> 5;
+    float a[16], x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const floatx4 v = *reinterpret_cast<const floatx4*>(A + (16 * b + r) * kLdA + 16 * b + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[4 * i + e] = v[e];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = r == 8 * h + j ? 1.f : 0.f;
+    substitute<0>(a, x);
+    float* t = tmp + (16 * b + r) * kLdT + 8 * h;
+    *reinterpret_cast<floatx4*>(t) = floatx4{x[0], x[1], x[2], x[3]};
+    *reinterpret_cast<floatx4*>(t + 4) = floatx4{x[4], x[5], x[6], x[7]};
+    {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = REV ? x[7 - j] : x[j];
+        const Planes<3> p = split8<3>(y);
+        const int row = 16 * b + r, piece = 2 * b + h;
+        const int at = REV ? square_at(31 - row, 3 - piece) : square_at(row, piece);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(out + n * C * C + at) = p.p[n];
+    }
+    wave_lds_fence();
+    const int m = lane & 15, g = lane >> 4;
+    const floatx4 a10 = *reinterpret_cast<const floatx4*>(A + (16 + m) * kLdA + 4 * g);
+    floatx4 w = {0.f, 0.f, 0.f, 0.f}, z = w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w = Mma<float>::mma(a10[i], tmp[(4 * g + i) * kLdT + m], w);
+    const floatx4 t1 = *reinterpret_cast<const floatx4*>(tmp + (16 + m) * kLdT + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z = Mma<float>::mma(w[i], t1[i], z);
+    // z: column m is row 16 + m of the inverse, its rows 4 g + 0..3 are columns
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = -(REV ? z[3 - e] : z[e]);
+    uint2 p[3];
+    split4<3>(y, p);
+    const int row = REV ? 15 - m : 16 + m, col = REV ? 28 - 4 * g : 4 * g;
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+        *reinterpret_cast<uint2*>(out + n * C * C + square_at(row, col >> 3) + (col & 7)) = p[n];
+}
+
+// ------------------------------------------------------------- a chunk's LDS, and helpers
+// E: element type of the inputs (planes: 1 for bfloat16, 3 for float32); W: waves that
+// carry the recurrence, 16 columns of d_v each.
+template <typename E, int DK_, int W_> struct Cfg {
+    static constexpr int NP = sizeof(E) == 2 ? 1 : 3;  // planes of an input
+    static constexpr int PP = sizeof(E) == 2 ? 2 : 3;  // planes behind the read-out, which is rounded to E
+    static constexpr int DK = DK_, W = W_, KT = DK / 16, KS = DK / 32;
+    static constexpr int NH = 4;  // helper waves
+    static constexpr int kThreads = 64 * (W + NH);
+    static constexpr int COLS = 16 * W;
+    static constexpr int LDV = COLS + (sizeof(E) == 2 ? 8 : 4);
+    static constexpr int LDO = COLS + 8;  // planes of dO
+    using Tile = Rows<DK>;
+};
+
+// eight elements of a row, or zeros, raw
+template <typename E> struct Raw8 {
+    static constexpr int N = sizeof(E) / 2;
+    u32x4 w[N];
+};
+template <typename E> __device__ __forceinline__ Raw8<E> load_raw8(const E* p, bool ok) {
+    Raw8<E> r;
+#pragma unroll
+    for (int i = 0; i < Raw8<E>::N; ++i) r.w[i] = ok ? reinterpret_cast<const u32x4*>(p)[i] : u32x4{0, 0, 0, 0};
+    return r;
+}
+template <typename E> __device__ __forceinline__ Planes<sizeof(E) == 2 ? 1 : 3> planes_of(const Raw8<E>& r) {
+    if constexpr (sizeof(E) == 2) {
+        return Planes<1>{{__builtin_bit_cast(bf16x8, r.w[0])}};
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i / 4][i % 4]);
+        return split8<3>(f);
+    }
+}
+
+// Token rows x[row0 + 0..31][0..D) on their way to LDS through the helper waves'
+// registers: thread `h` of 64 NH holds N pieces.
+template <typename E, int D, int THREADS> struct Stage {
+    static constexpr int kPer = D / 8, kAll = C * kPer, N = (kAll + THREADS - 1) / THREADS;
+    Raw8<E> r[N];
+    __device__ __forceinline__ void load(const E* x, size_t stride, int rows, int h) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = h + THREADS * i, row = e / kPer, p = e % kPer;
+            r[i] = load_raw8<E>(x + size_t(row) * stride + 8 * p, e < kAll && row < rows);
+        }
+    }
+    template <typename F> __device__ __forceinline__ void each(int h, F f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = h + THREADS * i;
+            if (kAll % THREADS == 0 || e < kAll) f(r[i], e / kPer, e % kPer);
+        }
+    }
+};
+
+// k_t.k_s (or q_t.k_s) of a 16 x 16 block: rows r0 of x against columns c0 of y
+template <typename Cf, int LIM>
+__device__ __forceinline__ floatx4 dots(const bf16_t* x, int r0, const bf16_t* y, int c0, int lane) {
+    constexpr int NP = Cf::NP;
+    using T = typename Cf::Tile;
+    const int m = lane & 15, g = lane >> 4;
+    floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < Cf::KS; ++j) {
+        Planes<NP> a, b;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            a.p[n] = T::row(x + n * C * Cf::DK, r0 + m, 4 * j + g);
+            b.p[n] = T::row(y + n * C * Cf::DK, c0 + m, 4 * j + g);
+        }
+        c = product<LIM>(a, b, c);
+    }
+    return c;
+}
+
+// The system's strictly lower triangle, A_ts = Gamma_ts k_t.k_s scaled by beta_s (its
+// columns; the forward pass) or, with REV, by beta_t and stored transposed and reversed
+// (the backward pass solves the transposed system).  G and beta [32] in LDS.
+template <typename Cf, bool REV>
+__device__ __forceinline__ void system_of(const bf16_t* k, const LogSum* G, const float* beta, float* A, int lane) {
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        const int bt = x == 0 ? 0 : 1, bs = x == 2 ? 1 : 0;  // blocks (0,0), (1,0), (1,1)
+        if constexpr (!REV) {
+            // rows are s = 16 bs + 4 g + e, this lane's column is t
+            const floatx4 d = dots<Cf, 2>(k, 16 * bs, k, 16 * bt, lane);
+            const int t = 16 * bt + m, s0 = 16 * bs + 4 * g;
+            floatx4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = s0 + e < t ? d[e] * decay_between(G[t], G[s0 + e]) * beta[s0 + e] : 0.f;
+            *reinterpret_cast<floatx4*>(A + t * kLdA + s0) = v;
+        } else {
+            // rows are t = 16 bt + 4 g + e, this lane's column is s
+            const floatx4 d = dots<Cf, 2>(k, 16 * bt, k, 16 * bs, lane);
+            const int s = 16 * bs + m, t0 = 16 * bt + 4 * g;
+            floatx4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[3 - e] = s < t0 + e ? d[e] * decay_between(G[t0 + e], G[s]) * beta[t0 + e] : 0.f;
+            *reinterpret_cast<floatx4*>(A + (31 - s) * kLdA + 28 - t0) = v;
+        }
+    }
+}
+
+// P_ts = scale Gamma_ts q_t.k_s (s <= t) in NPL planes of 32 x 32, or transposed.  The
+// block above the diagonal (below, transposed) must hold zeros already.
+template <typename Cf, bool TRANSPOSED, int NPL>
+__device__ __forceinline__ void readout_of(const bf16_t* q, const bf16_t* k, const LogSum* G, float scale, bf16_t* out,
+                                           int lane) {
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+        const int bt = x == 0 ? 0 : 1, bs = x == 2 ? 1 : 0;
+        float v[4];
+        int row, col;
+        if constexpr (!TRANSPOSED) {
+            const floatx4 d = dots<Cf, NPL - 1>(k, 16 * bs, q, 16 * bt, lane);
+            const int t = 16 * bt + m, s0 = 16 * bs + 4 * g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = s0 + e <= t ? scale * d[e] * decay_between(G[t], G[s0 + e]) : 0.f;
+            row = t;
+            col = s0;
+        } else {
+            const floatx4 d = dots<Cf, NPL - 1>(q, 16 * bt, k, 16 * bs, lane);
+            const int s = 16 * bs + m, t0 = 16 * bt + 4 * g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = s <= t0 + e ? scale * d[e] * decay_between(G[t0 + e], G[s]) : 0.f;
+            row = s;
+            col = t0;
+        }
+        uint2 p[NPL];
+        split4<NPL>(v, p);
+#pragma unroll
+        for (int n = 0; n < NPL; ++n)
+            *reinterpret_cast<uint2*>(out + n * C * C + square_at(row, col >> 3) + (col & 7)) = p[n];
+    }
+}
+
+// operand rows (paired_row) of a 32 x 32 matrix: its whole contraction in one step
+template <int N> __device__ __forceinline__ Planes<N> square_frag(const bf16_t* x, int h, int lane) {
+    const int at = square_at(paired_row(lane, h), lane >> 4);
+    Planes<N> r;
+#pragma unroll
+    for (int n = 0; n < N; ++n) r.p[n] = *reinterpret_cast<const bf16x8*>(x + n * C * C + at);
+    return r;
+}
+
+template <typename Cf>
+__device__ __forceinline__ Planes<Cf::NP> row_frag(const bf16_t* x, int h, int j, int lane) {
+    Planes<Cf::NP> r;
+    const int row = paired_row(lane, h);
+#pragma unroll
+    for (int n = 0; n < Cf::NP; ++n) r.p[n] = Cf::Tile::row(x + n * C * Cf::DK, row, 4 * j + (lane >> 4));
+    return r;
+}
+template <typename Cf>
+__device__ __forceinline__ Planes<Cf::NP> col_frag(const bf16_t* x, int j, int h, int lane) {
+    Planes<Cf::NP> r;
+#pragma unroll
+    for (int n = 0; n < Cf::NP; ++n) r.p[n] = Cf::Tile::col(x + n * C * Cf::DK, 0, j, h, lane);
+    return r;
+}
+
+// planes of the state for contraction step j: this lane's eight key dimensions
+template <int KT> __device__ __forceinline__ Planes<3> state_planes(const floatx4 (&st)[KT], int j) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[e] = st[2 * j][e];
+        f[4 + e] = st[2 * j + 1][e];
+    }
+    return split8<3>(f);
+}
+
+// state rows [d_v][d_k] float32: this lane's column n, eight key dimensions per step
+template <int KS> __device__ __forceinline__ void load_state(floatx4* st, const float* S, size_t col, int lane) {
+    const float* p = S + col * (32 * KS) + 8 * (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+        st[2 * j] = *reinterpret_cast<const floatx4*>(p + 32 * j);
+        st[2 * j + 1] = *reinterpret_cast<const floatx4*>(p + 32 * j + 4);
+    }
+}
+template <int KS> __device__ __forceinline__ void store_state(const floatx4* st, float* S, size_t col, int lane) {
+    float* p = S + col * (32 * KS) + 8 * (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+        *reinterpret_cast<floatx4*>(p + 32 * j) = st[2 * j];
+        *reinterpret_cast<floatx4*>(p + 32 * j + 4) = st[2 * j + 1];
+    }
+}
+
+// A state kept for the gradient kernel, in the order of its operand fragments (the
+// contraction runs over d_v): element (n, d) at
+//   ((n / 32) (DK / 16) + d / 16) 512 + (16 ((n % 32) / 8) + d % 16) 8 + n % 8
+template <typename E, int KS> __device__ __forceinline__ void keep_state(const floatx4* st, E* out, int n, int lane) {
+#pragma unroll
+    for (int j = 0; j < KS; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int d = 32 * j + 8 * (lane >> 4) + e;
+            const size_t at = size_t((n >> 5) * (2 * KS) + (d >> 4)) * 512 + (16 * ((n & 31) >> 3) + (d & 15)) * 8 + (n & 7);
+            out[at] = from_f<E>(st[2 * j + e / 4][e % 4]);
+        }
+}
+
+// where the states at group gr of a sequence are kept (see group_count); `per` tokens a
+// group.  Packed sequences: start / per + b is past every group of the sequences before.
+__device__ __forceinline__ size_t group_slot(const int32_t* cu, int b, int start, int per, int groups_of_T) {
+    return cu != nullptr ? size_t(start / per + b) : size_t(b) * groups_of_T;
+}
+
+// Workgroups are dealt to the 8 XCDs in turn: this order gives each XCD a run of
+// neighbours, which share q and k (the slices of a head, the heads of a group) in its L2.
+__device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned n) {
+    const unsigned x = id & 7u, y = id >> 3, q = n >> 3, r = n & 7u;
+    return x * q + min(x, r) + y;
+}
+
+}  // namespace delta
+}  // namespace kdn

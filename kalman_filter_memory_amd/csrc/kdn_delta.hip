@@ -1,0 +1,456 @@
+// kdn_delta.hip -- the gated delta rule over a sequence,
+//   S_t = e^g_t S_{t-1} + beta_t (v_t - e^g_t S_{t-1} k_t) k_t^T,   o_t = scale S_t q_t,
+// and one token of it on a cache of states (the mathematics of a chunk: kdn_delta.h).
+#include "kdn_delta.h"
+#include "kdn_delta_launch.h"
+
+namespace kdn {
+namespace delta {
+namespace {
+
+// The recurrence over the chunks of one (sequence, head): per chunk, from the state S,
+//   E = T (V - gamma K S),  U = beta E,  o = scale gamma Q S + P U,
+//   S <- gamma_C S + K^T (gamma_C / gamma U)
+// The columns of S are independent, so a wave carries 16 of them through the sequence
+// alone, in registers; the results of one product are the operands of the next without
+// any exchange (paired_row).  Four more waves load the chunks into LDS and prepare T and
+// P a chunk ahead, which do not depend on the state.
+// KEEP: instead of o, the corrections E and the states that the backward pass needs.
+template <typename E, int DK, int W, bool KEEP> struct ForwardLds {
+    using Cf = Cfg<E, DK, W>;
+    bf16_t k[2][Cf::NP * C * DK];
+    bf16_t q[KEEP ? 1 : 2][KEEP ? 8 : Cf::NP * C * DK];
+    E v[2][C * Cf::LDV];
+    bf16_t t[2][3 * C * C];
+    bf16_t p[KEEP ? 1 : 2][KEEP ? 8 : Cf::PP * C * C];
+    float a[C * kLdA];
+    float tmp[32 * kLdT];
+    float gam[2][C], rest[2][C], beta[2][C];
+    LogSum G[2][C];
+    float gb[C];  // of the wave that inverts, of the one that prepares P
+};
+
+template <typename E, int DK, int W, bool KEEP>
+__global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kernel(ForwardArgs a) {
+    using Cf = Cfg<E, DK, W>;
+    constexpr int NP = Cf::NP, PP = Cf::PP, KT = Cf::KT, KS = Cf::KS, HT = 64 * Cf::NH;
+    __shared__ __align__(16) ForwardLds<E, DK, W, KEEP> L;
+
+    const unsigned slices = unsigned(a.dv) / Cf::COLS;
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
+    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int nc = (sq.len + C - 1) / C;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int col0 = slice * Cf::COLS;
+    const size_t state = (size_t(b) * a.H + h) * size_t(a.dv) * DK;
+
+    const E* q = static_cast<const E*>(a.q) + sq.rq * DK;
+    const E* k = static_cast<const E*>(a.k) + sq.rq * DK;
+    const E* v = static_cast<const E*>(a.v) + sq.rv * a.dv + col0;
+
+    // zeros: the halves of T and P that no wave writes
+    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += Cf::kThreads)
+        reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
+    if constexpr (!KEEP)
+        for (unsigned i = threadIdx.x; i < 2 * PP * C * C / 8; i += Cf::kThreads)
+            reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
+    sync_lds();
+
+    if (wave >= W) {
+        // ------------------------------------------------------------------ helpers
+        const int ht = threadIdx.x - 64 * W, hw = wave - W;
+        Stage<E, DK, HT> sk, sq_;
+        Stage<E, Cf::COLS, HT> sv;
+        float g = 0.f, be = 0.f;
+        auto load = [&](int c) {
+            const int t0 = c * C, rows = sq.len - t0;
+            sk.load(k + size_t(t0) * DK, DK, rows, ht);
+            if constexpr (!KEEP) sq_.load(q + size_t(t0) * DK, DK, rows, ht);
+            sv.load(v + size_t(t0) * a.dv, a.dv, rows, ht);
+        };
+        auto gates = [&](int c) {  // of chunk c, token lane % 32
+            const int t = c * C + (lane & 31);
+            g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
+            be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
+        };
+        auto put = [&](int c) {
+            const int s = c & 1;
+            sk.each(ht, [&](const Raw8<E>& r, int row, int p) {
+                const auto x = planes_of<E>(r);
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    *reinterpret_cast<bf16x8*>(L.k[s] + n * C * DK + Cf::Tile::at(row, p)) = x.p[n];
+            });
+            if constexpr (!KEEP)
+                sq_.each(ht, [&](const Raw8<E>& r, int row, int p) {
+                    const auto x = planes_of<E>(r);
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        *reinterpret_cast<bf16x8*>(L.q[s] + n * C * DK + Cf::Tile::at(row, p)) = x.p[n];
+                });
+            sv.each(ht, [&](const Raw8<E>& r, int row, int p) {
+#pragma unroll
+                for (int i = 0; i < Raw8<E>::N; ++i)
+                    reinterpret_cast<u32x4*>(L.v[s] + row * Cf::LDV + 8 * p)[i] = r.w[i];
+            });
+        };
+        auto prepare = [&](int c) {  // T, or P and the gates, of chunk c
+            const int s = c & 1;
+            const LogSum G = log_sums(g, lane);
+            if (hw == 0) {
+                if (lane < C) {
+                    L.G[0][lane] = G;
+                    L.gb[lane] = be;
+                }
+                wave_lds_fence();
+                system_of<Cf, false>(L.k[s], L.G[0], L.gb, L.a, lane);
+                wave_lds_fence();
+                invert<false>(L.a, L.tmp, L.t[s], lane);
+            } else if (hw == 1) {
+                const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
+                if (lane < C) {
+                    L.G[1][lane] = G;
+                    L.gam[s][lane] = decay_of(G);
+                    L.rest[s][lane] = decay_between(last, G);
+                    L.beta[s][lane] = be;
+                }
+                if constexpr (!KEEP) {
+                    wave_lds_fence();
+                    readout_of<Cf, false, PP>(L.q[s], L.k[s], L.G[1], a.scale, L.p[s], lane);
+                }
+            }
+        };
+        if (nc > 0) {
+            load(0);
+            gates(0);
+            put(0);
+            if (nc > 1) load(1);
+        }
+        sync_lds();
+        if (nc > 0) prepare(0);
+        if (nc > 1) {
+            gates(1);
+            put(1);
+        }
+        sync_lds();
+        for (int c = 0; c < nc; ++c) {
+            if (c + 2 < nc) load(c + 2);
+            if (c + 1 < nc) {
+                prepare(c + 1);
+                if (c + 2 < nc) gates(c + 2);
+            }
+            sync_lds();  // chunk c is done with
+            if (c + 2 < nc) put(c + 2);
+            sync_lds();
+        }
+        return;
+    }
+
+    // --------------------------------------------------------------------- recurrence
+    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
+    floatx4 st[KT];
+    if (a.S0 != nullptr) {
+        load_state<KS>(st, a.S0 + state, col, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    const size_t groups = KEEP ? group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) : 0;
+    sync_lds();
+    sync_lds();
+    for (int c = 0; c < nc; ++c) {
+        const int s = c & 1;
+        if constexpr (KEEP) {
+            if (c % a.group == 0)
+                keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col,
+                                  lane);
+        }
+        // K S (and Q S)
+        floatx4 ks[2], qs[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            const Planes<3> sp = state_planes<KT>(st, j);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ks[x] = product<2>(row_frag<Cf>(L.k[s], x, j, lane), sp, ks[x]);
+            if constexpr (!KEEP)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) qs[x] = product<PP - 1>(row_frag<Cf>(L.q[s], x, j, lane), sp, qs[x]);
+        }
+        // E = T (V - gamma K S); this lane's tokens are 8 g + 0..7 of the chunk
+        floatx4 gam[2], be[2], rest[2];
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t = 8 * g + 4 * x;
+            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
+            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[s][t]);
+            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
+            float vv[4];
+            if constexpr (sizeof(E) == 2) {
+                const short4x w = read_tr16(L.v[s] + (t + (m >> 2)) * Cf::LDV + 16 * wave + 4 * (lane & 3));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) vv[e] = bf2f(static_cast<bf16_t>(w[e]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) vv[e] = L.v[s][(t + e) * Cf::LDV + 16 * wave + m];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * x + e] = vv[e] - gam[x][e] * ks[x][e];
+        }
+        const Planes<3> rp = split8<3>(f);
+        floatx4 ee[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            ee[x] = product<2>(square_frag<3>(L.t[s], x, lane), rp, floatx4{0.f, 0.f, 0.f, 0.f});
+        float u[8], ub[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                u[4 * x + e] = be[x][e] * ee[x][e];
+                ub[4 * x + e] = rest[x][e] * u[4 * x + e];
+            }
+        // S <- gamma_C S + K^T (rest U)
+        const Planes<3> up = split8<3>(ub);
+        const float last = L.gam[s][C - 1];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const floatx4 w = {last * st[i][0], last * st[i][1], last * st[i][2], last * st[i][3]};
+            st[i] = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), up, w);
+        }
+        const int rows = sq.len - c * C;
+        if constexpr (KEEP) {
+            E* out = static_cast<E*>(a.keep_E) + (sq.rv + size_t(c) * C) * a.dv + col;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * g + 4 * x + e;
+                    if (t < rows) out[size_t(t) * a.dv] = from_f<E>(ee[x][e]);
+                }
+        } else {
+            const Planes<PP> uo = split8<PP>(u);
+            E* out = static_cast<E*>(a.o) + (sq.rv + size_t(c) * C) * a.dv + col;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                floatx4 o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = a.scale * gam[x][e] * qs[x][e];
+                o = product<PP - 1>(square_frag<PP>(L.p[s], x, lane), uo, o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * g + 4 * x + e;
+                    if (t < rows) out[size_t(t) * a.dv] = from_f<E>(o[e]);
+                }
+            }
+        }
+        sync_lds();
+        sync_lds();
+    }
+    if (a.S_T != nullptr) store_state<KS>(st, a.S_T + state, col, lane);
+}
+
+template <typename E, int DK, int W>
+void forward_dw(const ForwardArgs& a, bool keep, hipStream_t st) {
+    const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(a.dv / (16 * W));
+    constexpr int threads = Cfg<E, DK, W>::kThreads;
+    if (keep) delta_forward_kernel<E, DK, W, true><<<n, threads, 0, st>>>(a);
+    else delta_forward_kernel<E, DK, W, false><<<n, threads, 0, st>>>(a);
+}
+template <typename E, int DK> void forward_d(const ForwardArgs& a, bool keep, hipStream_t st) {
+    if (a.dv == 32) forward_dw<E, DK, 2>(a, keep, st);
+    else forward_dw<E, DK, 4>(a, keep, st);
+}
+template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hipStream_t st) {
+    if (dk == 32) forward_d<E, 32>(a, keep, st);
+    else if (dk == 64) forward_d<E, 64>(a, keep, st);
+    else forward_d<E, 128>(a, keep, st);
+}
+
+// ------------------------------------------------------------------------- one token
+// d_k / 4 lanes per row of S, four elements each; a workgroup owns one state, every wave
+// d_v / NW of its rows.  Bound by the state's 8 d_k d_v bytes.
+template <int DK, int DV> struct StepCfg {
+    static constexpr int LPR = DK / 4, RPS = 64 / LPR;
+    static constexpr int NW = DV / RPS < 8 ? DV / RPS : 8, RPW = DV / NW, SLOTS = RPW / RPS;
+};
+
+template <typename E, typename G, int DK, int DV>
+__global__ __launch_bounds__((64 * StepCfg<DK, DV>::NW)) void delta_step_kernel(
+    const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v, const G* __restrict__ gate,
+    const G* __restrict__ beta, float* __restrict__ S, const int32_t* __restrict__ slot, int H, int Hk, int n_slots,
+    float scale, E* __restrict__ o) {
+    using Cf = StepCfg<DK, DV>;
+    constexpr int LPR = Cf::LPR, SLOTS = Cf::SLOTS;
+    const unsigned st = blockIdx.x;
+    const int b = int(st / unsigned(H)), h = int(st % unsigned(H));
+    size_t at = st;
+    if (slot != nullptr) {
+        const int s = slot[b];
+        if (s < 0 || s >= n_slots) return;
+        at = size_t(s) * H + h;
+    }
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int col = 4 * (lane % LPR), row0 = wave * Cf::RPW + lane / LPR;
+    float* Sp = S + at * size_t(DK * DV) + col;
+    const size_t hk = size_t(b) * Hk + h / (H / Hk);
+    float kv[4], qv[4], vj[SLOTS];
+    floatx4 s[SLOTS];
+    const float gt = to_f<G>(gate[st]), bt = to_f<G>(beta[st]);
+    load_vec<E, 4>(k + hk * DK + col, kv);
+    load_vec<E, 4>(q + hk * DK + col, qv);
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) vj[i] = to_f<E>(v[size_t(st) * DV + row0 + i * Cf::RPS]);
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) s[i] = *reinterpret_cast<const floatx4*>(Sp + (row0 + i * Cf::RPS) * DK);
+    __builtin_amdgcn_sched_barrier(0);  // the state's loads go first
+    const float a = exp2_hw(float(log2_decay(gt)));
+    float kq = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kq += kv[i] * qv[i];
+    kq = group_sum<LPR>(kq);
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+        const int row = row0 + i * Cf::RPS;
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sk = fmaf(s[i][e], kv[e], sk);
+            sq = fmaf(s[i][e], qv[e], sq);
+        }
+        sk = group_sum<LPR>(sk);
+        sq = group_sum<LPR>(sq);
+        const float u = bt * (vj[i] - a * sk);
+        floatx4 n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n[e] = fmaf(u, kv[e], a * s[i][e]);
+        *reinterpret_cast<floatx4*>(Sp + row * DK) = n;
+        if (col == 0) o[size_t(st) * DV + row] = from_f<E>(scale * (a * sq + u * kq));
+    }
+}
+
+struct StepArgs {
+    const void *q, *k, *v, *g, *beta;
+    float* S;
+    const int32_t* slot;
+    void* o;
+    int H, Hk, n_slots;
+    float scale;
+};
+template <typename E, typename G, int DK, int DV> void step_go(const StepArgs& a, unsigned n, hipStream_t st) {
+    delta_step_kernel<E, G, DK, DV><<<n, 64 * StepCfg<DK, DV>::NW, 0, st>>>(
+        static_cast<const E*>(a.q), static_cast<const E*>(a.k), static_cast<const E*>(a.v), static_cast<const G*>(a.g),
+        static_cast<const G*>(a.beta), a.S, a.slot, a.H, a.Hk, a.n_slots, a.scale, static_cast<E*>(a.o));
+}
+template <typename E, typename G, int DK> void step_dv(const StepArgs& a, int dv, unsigned n, hipStream_t st) {
+    if (dv == 32) step_go<E, G, DK, 32>(a, n, st);
+    else if (dv == 64) step_go<E, G, DK, 64>(a, n, st);
+    else step_go<E, G, DK, 128>(a, n, st);
+}
+template <typename E, typename G> void step_dk(const StepArgs& a, int dk, int dv, unsigned n, hipStream_t st) {
+    if (dk == 32) step_dv<E, G, 32>(a, dv, n, st);
+    else if (dk == 64) step_dv<E, G, 64>(a, dv, n, st);
+    else step_dv<E, G, 128>(a, dv, n, st);
+}
+
+// no tokens: the states pass through
+__global__ __launch_bounds__(256) void delta_states_kernel(size_t n, const float* in, float* out) {
+    const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) out[i] = in != nullptr ? in[i] : 0.f;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+kdn_status check(const kdn_delta_desc* d, bool one_token) {
+    if (!d) return KDN_ERR_NULL;
+    if (d->B < 0 || d->H < 0 || d->Hk < 0 || d->T < 0) return KDN_ERR_SHAPE;
+    if (d->H > 0 && (d->Hk == 0 || d->H % d->Hk != 0)) return KDN_ERR_SHAPE;
+    auto width = [](int x) { return x == 32 || x == 64 || x == 128; };
+    auto type = [](int t) { return t == KDN_F32 || t == KDN_BF16; };
+    if (!width(d->d_k) || !width(d->d_v) || !type(d->dtype) || !type(d->gate_dtype)) return KDN_ERR_UNSUPPORTED;
+    if (!(d->scale == d->scale) || d->scale - d->scale != 0.f) return KDN_ERR_SHAPE;
+    if (int64_t(d->B) * d->H > kMaxStates || (!one_token && d->T > kMaxTokens)) return KDN_ERR_UNSUPPORTED;
+    return KDN_OK;
+}
+
+hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st) {
+    if (dtype == KDN_BF16) forward_e<bf16_t>(a, dk, keep, st);
+    else forward_e<float>(a, dk, keep, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st) {
+    if (n == 0 || out == nullptr || in == out) return hipSuccess;
+    delta_states_kernel<<<unsigned((n + 255) / 256), 256, 0, st>>>(n, in, out);
+    return hipGetLastError();
+}
+
+}  // namespace delta
+}  // namespace kdn
+
+extern "C" {
+
+size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc* d) {
+    return kdn::delta::check(d, false) == KDN_OK ? 16 : 0;
+}
+
+kdn_status kdn_gated_delta(const kdn_delta_desc* d, const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
+                           const void* g, const void* beta, const float* S0, void* o, float* S_T, void* ws,
+                           size_t ws_bytes, void* stream) {
+    using namespace kdn::delta;
+    const kdn_status c = check(d, false);
+    if (c != KDN_OK) return c;
+    if (d->B == 0 || d->H == 0) return KDN_OK;
+    for (const void* p : {q, k, v, (const void*)S0, (const void*)o, (const void*)S_T, (const void*)ws})
+        if (!aligned16(p)) return KDN_ERR_ALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (d->T == 0)
+        return launch_states(size_t(d->B) * d->H * d->d_k * d->d_v, S0, S_T, st) == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+    if (!q || !k || !v || !g || !beta || !o) return KDN_ERR_NULL;
+    ForwardArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.beta = beta;
+    a.cu = cu_seqlens;
+    a.S0 = S0;
+    a.o = o;
+    a.S_T = S_T;
+    a.B = d->B;
+    a.H = d->H;
+    a.Hk = d->Hk;
+    a.T = d->T;
+    a.dv = d->d_v;
+    a.scale = d->scale;
+    a.gate_bf16 = d->gate_dtype == KDN_BF16;
+    return launch_forward(a, d->dtype, d->d_k, false, st) == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+}
+
+kdn_status kdn_gated_delta_step(const kdn_delta_desc* d, const void* q, const void* k, const void* v, const void* g,
+                                const void* beta, float* S, const int32_t* slot, int32_t n_slots, void* o, void* stream) {
+    using namespace kdn::delta;
+    const kdn_status c = check(d, true);
+    if (c != KDN_OK) return c;
+    if (n_slots < 0) return KDN_ERR_SHAPE;
+    if (d->B == 0 || d->H == 0) return KDN_OK;
+    if (!q || !k || !v || !g || !beta || !S || !o) return KDN_ERR_NULL;
+    for (const void* p : {q, k, (const void*)S})
+        if (!aligned16(p)) return KDN_ERR_ALIGN;
+    const StepArgs a{q, k, v, g, beta, S, slot, o, d->H, d->Hk, n_slots, d->scale};
+    const unsigned n = unsigned(d->B) * unsigned(d->H);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool xf = d->dtype == KDN_F32, gf = d->gate_dtype == KDN_F32;
+    if (xf && gf) step_dk<float, float>(a, d->d_k, d->d_v, n, st);
+    else if (xf) step_dk<float, kdn::bf16_t>(a, d->d_k, d->d_v, n, st);
+    else if (gf) step_dk<kdn::bf16_t, float>(a, d->d_k, d->d_v, n, st);
+    else step_dk<kdn::bf16_t, kdn::bf16_t>(a, d->d_k, d->d_v, n, st);
+    return hipGetLastError() == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,37 @@
+// kdn_delta_launch.h -- arguments and launchers that the gated delta rule's forward and
+// backward passes share (host side, internal).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/kdn.h"
+
+namespace kdn {
+namespace delta {
+
+// workgroups of a launch stay below 2^32 with four slices of a head, and below the
+// 2^32 threads of a grid with 512 each
+constexpr int64_t kMaxStates = (1 << 20) - 1;
+constexpr int32_t kMaxTokens = 1 << 30;
+
+struct ForwardArgs {
+    const void *q, *k, *v, *g, *beta;
+    const int32_t* cu;  // packed sequences' first rows [B + 1], or null
+    const float* S0;
+    void* o;
+    float* S_T;
+    void *keep_E, *keep_S;  // for the backward pass
+    int B, H, Hk, T, dv;
+    int group;  // chunks per kept state
+    float scale;
+    bool gate_bf16;
+};
+
+kdn_status check(const kdn_delta_desc* d, bool one_token);
+hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st);
+hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st);
+
+}  // namespace delta
+}  // namespace kdn
