@@ -616,6 +616,28 @@ kdn_status kdn_gated_delta(const kdn_delta_desc *d, const int32_t *cu_seqlens, c
                            const float *S0, void *o, float *S_T, void *ws, size_t ws_bytes,
                            void *stream);
 
+/* Its backward: gradients of <dO, o> + <dS_T, S_T> (dS_T NULL: zeros), from the
+ * inputs of the forward (nothing is kept between the calls):
+ *   dq, dk [B,Hk,T,d_k]  sums over the heads of values that share them
+ *   dv [B,H,T,d_v]; dg, dbeta [B,H,T]   all in dtype, whatever the gates' type
+ *   dS0 [B,H,d_v,d_k] float32 (NULL skips it)
+ * laid out as the inputs, packed ones too (rows in no sequence are not written).
+ * Sums are float32 in a fixed order: the same call gives the same bits.  In
+ * bfloat16 the operands of the last products (corrections, states at every 64th
+ * token, dv and their weights) are rounded to bfloat16, which costs dq, dk, dg and
+ * dbeta a few of their own roundings; dv and dS0 carry none of it.  dS0 may be
+ * dS_T's buffer; no other output may alias an input.  Fewer than 2^23 groups of 64
+ * tokens (float32: 32) of all heads of keys (KDN_ERR_UNSUPPORTED otherwise).
+ * packed: whether cu_seqlens will be given.  Every pointer but g, beta, dg, dbeta
+ * and cu_seqlens 16-byte aligned. */
+size_t kdn_gated_delta_backward_workspace_bytes(const kdn_delta_desc *d, int32_t packed);
+kdn_status kdn_gated_delta_backward(const kdn_delta_desc *d, const int32_t *cu_seqlens,
+                                    const void *q, const void *k, const void *v, const void *g,
+                                    const void *beta, const float *S0, const void *dO,
+                                    const float *dS_T, void *dq, void *dk, void *dv, void *dg,
+                                    void *dbeta, float *dS0, void *ws, size_t ws_bytes,
+                                    void *stream);
+
 /* One token in place: q, k [B,Hk,d_k]; v, o [B,H,d_v]; g, beta [B,H]; S
  * [B,H,d_v,d_k] is read and overwritten.  d->T is not used.  slot NULL, or device
  * int32 [B]: S is then a cache [n_slots,H,d_v,d_k] and sequence b's state is at

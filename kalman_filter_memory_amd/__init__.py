@@ -32,6 +32,8 @@ Functions (same names as the C entry points):
   gated_delta(q, k, v, g, beta, S0=None) -> (o, S_T)      (the gated delta rule)
   gated_delta_varlen(q, k, v, g, beta, cu_seqlens, S0=None) -> (o, S_T)   (a packed batch)
   gated_delta_step(q, k, v, g, beta, S, slot=None) -> o   (one token, S in place)
+  gated_delta_backward(q, k, v, g, beta, dO, S0=None, dS_T=None, cu_seqlens=None) -> dict of
+                 gradients (dq, dk, dv, dg, dbeta in q's dtype, dS0 float32)
 """
 from __future__ import annotations
 
@@ -64,6 +66,7 @@ EXPORTS = (
     "kdn_gated_scan_workspace_bytes", "kdn_gated_scan_backward_workspace_bytes",
     "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
     "kdn_gated_delta_workspace_bytes", "kdn_gated_delta", "kdn_gated_delta_step",
+    "kdn_gated_delta_backward_workspace_bytes", "kdn_gated_delta_backward",
 )
 
 
@@ -185,6 +188,9 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_gated_delta_workspace_bytes.argtypes = [E]
     lib.kdn_gated_delta_workspace_bytes.restype = S
     lib.kdn_gated_delta.argtypes = [E] + [P] * 10 + [S, P]
+    lib.kdn_gated_delta_backward_workspace_bytes.argtypes = [E, ctypes.c_int32]
+    lib.kdn_gated_delta_backward_workspace_bytes.restype = S
+    lib.kdn_gated_delta_backward.argtypes = [E] + [P] * 16 + [S, P]
     lib.kdn_gated_delta_step.argtypes = [E] + [P] * 7 + [ctypes.c_int32, P, P]
     _lib = lib
     return lib
@@ -1054,6 +1060,39 @@ def gated_delta_varlen(q, k, v, g, beta, cu_seqlens, S0=None, scale=None, out=No
     if cu_seqlens is None:
         raise ValueError("cu_seqlens must be int32 [N+1]")
     return _gated_delta(q, k, v, g, beta, cu_seqlens, S0, scale, out)
+
+
+def gated_delta_backward(q, k, v, g, beta, dO, S0=None, dS_T=None, scale=None, cu_seqlens=None,
+                         out=None) -> dict:
+    """Gradients of <dO, o> + <dS_T, S_T> with respect to the inputs of gated_delta, or of
+    gated_delta_varlen with cu_seqlens, in a dict: dq, dk (summed over the heads of v that
+    share them), dv, dg and dbeta in q's dtype, dS0 float32.  dO [.., T, d_v] in q's dtype;
+    dS_T float32 [B,H,d_v,d_k] or None (zeros).  out: optional dict of preallocated outputs
+    with those keys (rows in no sequence are left as they were in it)."""
+    dev = _tensors(("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("dO", dO),
+                   ("S0", S0), ("dS_T", dS_T), ("cu_seqlens", cu_seqlens))
+    d = _delta_desc(q, k, v, g, beta, scale, cu_seqlens)
+    states = (d.B, d.H, d.d_v, d.d_k)
+    _shaped("dO", dO, v.dtype, v.shape)
+    _shaped("S0", S0, torch.float32, states)
+    _shaped("dS_T", dS_T, torch.float32, states)
+    like = {"dq": q, "dk": k, "dv": v, "dg": g, "dbeta": beta}
+    if out is None:
+        r = {n: torch.empty_like(x, dtype=q.dtype) for n, x in like.items()}
+        r["dS0"] = _empty(states, torch.float32, dev)
+    else:
+        r = {n: out[n] for n in (*like, "dS0")}
+        _tensors(("q", q), *r.items())
+        for n, x in like.items():
+            _shaped(n, r[n], q.dtype, x.shape)
+        _shaped("dS0", r["dS0"], torch.float32, states)
+    need = load_library().kdn_gated_delta_backward_workspace_bytes(ctypes.byref(d),
+                                                                   int(cu_seqlens is not None))
+    ws = _empty((max(need, 16),), torch.uint8, dev)
+    _launch("kdn_gated_delta_backward", dev, ctypes.byref(d), _ptr(cu_seqlens), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0), dO.data_ptr(),
+            _ptr(dS_T), *(r[n].data_ptr() for n in (*like, "dS0")), ws.data_ptr(), need)
+    return r
 
 
 def gated_delta_step(q, k, v, g, beta, S, slot=None, scale=None, out=None):

@@ -155,13 +155,13 @@ __device__ __forceinline__ double log2_decay(float g) {
     const double x = double(g) * 1.4426950408889634;
     return x < -160.0 ? -160.0 : x;
 }
-// inclusive sums over the 32 lanes of each half of a wave
-__device__ __forceinline__ LogSum log_sums(float g, int lane) {
+// inclusive sums over each N lanes of a wave
+template <int N> __device__ __forceinline__ LogSum log_sums(float g, int lane) {
     double x = log2_decay(g);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up(x, d, 32);
-        x += (lane & 31) >= d ? y : 0.0;
+    for (int d = 1; d < N; d <<= 1) {
+        const double y = __shfl_up(x, d, N);
+        x += (lane & (N - 1)) >= d ? y : 0.0;
     }
     const float hi = float(x);
     return LogSum{hi, float(x - double(hi))};
@@ -444,17 +444,15 @@ template <int KS> __device__ __forceinline__ void store_state(const floatx4* st,
 }
 
 // A state kept for the gradient kernel, in the order of its operand fragments (the
-// contraction runs over d_v): element (n, d) at
-//   ((n / 32) (DK / 16) + d / 16) 512 + (16 ((n % 32) / 8) + d % 16) 8 + n % 8
+// contraction runs over d_v; key dimensions in the order of paired_row): element (n, d)
+// with d = 32 j + 8 a + 4 h + b at
+//   ((n / 32) (DK / 16) + 2 j + h) 512 + (16 ((n % 32) / 8) + 4 a + b) 8 + n % 8
 template <typename E, int KS> __device__ __forceinline__ void keep_state(const floatx4* st, E* out, int n, int lane) {
+    E* p = out + (n >> 5) * (KS * 1024) + (16 * ((n & 31) >> 3) + 4 * (lane >> 4)) * 8 + (n & 7);
 #pragma unroll
-    for (int j = 0; j < KS; ++j)
+    for (int i = 0; i < 2 * KS; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int d = 32 * j + 8 * (lane >> 4) + e;
-            const size_t at = size_t((n >> 5) * (2 * KS) + (d >> 4)) * 512 + (16 * ((n & 31) >> 3) + (d & 15)) * 8 + (n & 7);
-            out[at] = from_f<E>(st[2 * j + e / 4][e % 4]);
-        }
+        for (int e = 0; e < 4; ++e) p[i * 512 + e * 8] = from_f<E>(st[i][e]);
 }
 
 // where the states at group gr of a sequence are kept (see group_count); `per` tokens a

@@ -97,7 +97,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
         };
         auto prepare = [&](int c) {  // T, or P and the gates, of chunk c
             const int s = c & 1;
-            const LogSum G = log_sums(g, lane);
+            const LogSum G = log_sums<C>(g, lane);
             if (hw == 0) {
                 if (lane < C) {
                     L.G[0][lane] = G;

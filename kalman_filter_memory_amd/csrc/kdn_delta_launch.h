@@ -29,6 +29,14 @@ struct ForwardArgs {
     bool gate_bf16;
 };
 
+// What the backward pass keeps between its kernels: chunks per kept state, and places
+// for states (per head of values).
+inline int kept_chunks(int dtype) { return dtype == KDN_BF16 ? 2 : 1; }
+inline size_t kept_slots(const int32_t* cu, int B, int T, int group) {
+    const int per = 32 * group;
+    return cu != nullptr ? size_t(T / per) + B + 1 : size_t(B) * ((T + per - 1) / per);
+}
+
 kdn_status check(const kdn_delta_desc* d, bool one_token);
 hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st);
 hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st);

@@ -103,3 +103,54 @@ def inputs(B, H, Hk, T, dk, dv, dtype, gate, seed, kind="decay", device="cuda"):
         gate_ = torch.where(r > 1.5, -float("inf"), torch.where(r > 0, 0.0, gate_))
         beta = torch.where(rand(B, H, T) > 1, 0.0, torch.where(rand(B, H, T) > 1, 1.0, beta))
     return q, k, v, gate_.to(tg), beta.to(tg), rand(B, H, dv, dk)
+
+
+def _blocks(T, n):
+    return [(at, min(n, T - at)) for at in range(0, T, n)]
+
+
+def rounding_bounds(q, k, v, g, beta, do, S0, dS_T, half, scale=None):
+    """Bounds on what rounding the operands of the last products to a type with that half
+    step costs each element of dq, dk, dg and dbeta (in groups of 64 tokens): every product's
+    sum of absolute values, times the roundings on its way.  E, dV, S and D are rounded
+    once, U = beta E once more, and the weights dP and M behind U (and dV):
+      dO S: 1   dP K, dP Q: E, U, dP 3   M K: E, U, dV, M 4   U D: E, U, D 3   dV S: 2   X E: 1."""
+    H, T = v.shape[1], v.shape[2]
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    grads = delta_gradients(q, k, v, g, beta, do, S0, dS_T, scale)
+    _, _, kept = delta(q, k, v, g, beta, S0, scale)
+    Hk, r = q.shape[1], H // q.shape[1]
+    q, k, v, g, beta, do = (x.double() for x in (shared(q, H), shared(k, H), v, g, beta, do))
+    # e_t from the states: S_t - a S_{t-1} = u_t k_t^T
+    E, X = torch.zeros_like(v), torch.zeros_like(v)
+    D = [None] * (T + 1)
+    D[T] = torch.zeros_like(kept[0]) if dS_T is None else dS_T.double()
+    for t in reversed(range(T)):
+        old = kept[t] * g[:, :, t, None, None].exp()
+        E[:, :, t] = v[:, :, t] - (old * k[:, :, t, None, :]).sum(-1)
+        now = D[t + 1] + scale * do[:, :, t, :, None] * q[:, :, t, None, :]
+        X[:, :, t] = (now * k[:, :, t, None, :]).sum(-1)
+        D[t] = (now - (beta[:, :, t, None] * X[:, :, t])[..., None] * k[:, :, t, None, :]) * g[:, :, t, None, None].exp()
+    U, dv = (beta[..., None] * E).abs(), grads["dv"].abs()
+    out = {n: torch.zeros_like(x) for n, x in (("dq", q), ("dk", k), ("dg", g))}
+    out["dbeta"] = (X.abs() * E.abs()).sum(-1)
+    mm = lambda x, y: x @ y.contiguous()  # noqa: E731
+    for at, n in _blocks(T, 64):
+        sl = slice(at, at + n)
+        G = g[:, :, sl].clamp_min(-700).cumsum(-1)
+        gam, rest = G.exp()[..., None], (G[..., -1:] - G).exp()[..., None]
+        ratio = (G[..., :, None] - G[..., None, :]).tril().exp().tril()
+        Q, K, O, W, u = q[:, :, sl].abs(), k[:, :, sl].abs(), do[:, :, sl].abs(), dv[:, :, sl], U[:, :, sl]
+        S, De = kept[at].abs(), D[at + n].abs()
+        P, M = scale * mm(O, u.transpose(-1, -2)) * ratio, (mm(W, u.transpose(-1, -2)) * ratio).tril(-1)
+        os, vs, ud = scale * gam * mm(O, S), gam * mm(W, S), rest * mm(u, De)
+        out["dq"][:, :, sl] = os + 3 * mm(P, K)
+        out["dk"][:, :, sl] = 3 * mm(P.transpose(-1, -2), Q) + 4 * (mm(M, K) + mm(M.transpose(-1, -2), K)) + 3 * ud + 2 * vs
+        A, B = (Q * os).sum(-1) + 2 * (K * vs).sum(-1), 3 * (K * ud).sum(-1)
+        w = 3 * P * (q[:, :, sl] @ k[:, :, sl].transpose(-1, -2).contiguous()).abs() \
+            + 4 * M * (k[:, :, sl] @ k[:, :, sl].transpose(-1, -2).contiguous()).abs()
+        for t in range(n):
+            out["dg"][:, :, at + t] = (2 * (De * S).sum((-1, -2)) * gam[:, :, -1, 0] + A[:, :, t:].sum(-1) + B[:, :, :t].sum(-1)
+                                       + w[:, :, t:, :t].sum((-1, -2)))
+    out["dq"], out["dk"] = (out[n].unflatten(1, (Hk, r)).sum(2) for n in ("dq", "dk"))
+    return grads, {n: half * out[n] for n in out}

@@ -38,6 +38,9 @@ def test_refuses_descriptors(lib, kw, code):
     assert lib.kdn_gated_delta_workspace_bytes(d) == 0
     assert lib.kdn_gated_delta(d, None, *([FAKE] * 9), 1 << 40, None) == code
     assert lib.kdn_gated_delta_step(d, *([FAKE] * 6), None, 0, FAKE, None) == code
+    for packed in (0, 1):
+        assert lib.kdn_gated_delta_backward_workspace_bytes(d, packed) == 0
+    assert lib.kdn_gated_delta_backward(d, None, *([FAKE] * 15), 1 << 40, None) == code
 
 
 def test_refuses_too_many_tokens(lib):
@@ -70,6 +73,29 @@ def test_refuses_arguments(lib):
         args = [FAKE] * 6
         args[i] = ODD
         assert lib.kdn_gated_delta_step(d, *args, None, 0, FAKE, None) == 5
+
+
+def test_backward_refuses_arguments(lib):
+    d = ctypes.byref(_desc())
+    need = lib.kdn_gated_delta_backward_workspace_bytes(d, 0)
+    # E, states before and gradients behind each 64 tokens, a row of dbeta for 16 columns
+    assert need == 2 * 4 * 10 * 32 * 2 + 2 * (2 * 4 * 32 * 64 * 2) + 2 * 4 * 10 * 2 * 4 + 128 + 16
+    assert lib.kdn_gated_delta_backward_workspace_bytes(d, 1) > 0
+    assert lib.kdn_gated_delta_backward(d, None, *([FAKE] * 15), need - 1, None) == 4
+    assert lib.kdn_gated_delta_backward(None, None, *([FAKE] * 15), need, None) == 1
+    for i in (0, 1, 2, 3, 4, 6, 8, 9, 10, 11, 12, 14):  # not S0, dS_T, dS0
+        args = [FAKE] * 15
+        args[i] = None
+        assert lib.kdn_gated_delta_backward(d, None, *args, need, None) == 1
+    for i in (0, 1, 2, 5, 6, 7, 8, 9, 10, 13, 14):  # not g, beta, dg, dbeta
+        args = [FAKE] * 15
+        args[i] = ODD
+        assert lib.kdn_gated_delta_backward(d, None, *args, need, None) == 5
+    # more groups of tokens than a launch takes
+    many = ctypes.byref(_desc(B=1, H=16, Hk=16, T=1 << 26))
+    assert lib.kdn_gated_delta_backward_workspace_bytes(many, 0) == 0
+    assert lib.kdn_gated_delta_backward(many, None, *([FAKE] * 15), 1 << 60, None) == 3
+    assert lib.kdn_gated_delta_backward(ctypes.byref(_desc(B=0)), None, *([None] * 15), 0, None) == 0
 
 
 def test_nothing_to_do(lib):
