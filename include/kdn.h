@@ -648,6 +648,59 @@ kdn_status kdn_gated_delta_step(const kdn_delta_desc *d, const void *q, const vo
                                 const void *v, const void *g, const void *beta, float *S,
                                 const int32_t *slot, int32_t n_slots, void *o, void *stream);
 
+/* --------------------------------------- head norm and rotation by position
+ * What stands between a projection and a recurrence over heads: for every head row
+ * x of d columns of queries and keys
+ *   n = x (mean x^2 + eps)^(-1/2) weight                (RMS norm over the head)
+ *   y = n with the pairs of its first rot columns turned by position * inv_freq[i]:
+ *       (a, b) -> (a cos - b sin, b cos + a sin), the pair i being columns
+ *       (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved
+ * and token rows become head rows.  (The L2 norm of kdn_layer_forward is the weight
+ * d^(-1/2).)
+ *   q: head h of token t of sequence b at b q_stride[0] + t q_stride[1] + h
+ *      q_stride[2] elements, its columns contiguous (a view of a projection's rows)
+ *   q_out [B,H,T,d], q_rstd [B,H,T] float32 the inverse roots; k: the same, Hk heads
+ *   weights [d] and inv_freq [rot / 2] float32; position [B,T] int32 (any value)
+ * d a multiple of 8 up to 256, rot a multiple of 16 up to d (0: no rotation, position
+ * and inv_freq may be NULL), B*T below 2^26, H and Hk up to 2^16
+ * (KDN_ERR_UNSUPPORTED otherwise); strides multiples of 8 (KDN_ERR_ALIGN).  Angles
+ * are products in 64 bits: far positions keep float32's accuracy. */
+typedef struct {
+    int32_t B, T, H, Hk, d, rot;
+    int32_t dtype;       /* kdn_dtype of q, k and the outputs */
+    int32_t interleaved; /* pairs are neighbours */
+    float eps;
+    int64_t q_stride[3], k_stride[3];   /* batch, token, head; in elements */
+    int64_t dq_stride[3], dk_stride[3]; /* the backward's outputs, likewise */
+} kdn_rotary_desc;
+
+/* q_rstd, k_rstd: NULL or outputs.  No output may alias an input.  Pointers but
+ * position, inv_freq and the rstds 16-byte aligned. */
+kdn_status kdn_qk_norm_rotary(const kdn_rotary_desc *d, const void *q, const void *k,
+                              const float *q_weight, const float *k_weight,
+                              const int32_t *position, const float *inv_freq, void *q_out,
+                              void *k_out, float *q_rstd, float *k_rstd, void *stream);
+
+/* Bytes of workspace the backward needs (0 if the descriptor is invalid).
+ * Host-only. */
+size_t kdn_qk_norm_rotary_backward_workspace_bytes(const kdn_rotary_desc *d);
+
+/* Its backward: from dq_out, dk_out (the outputs' gradients, head rows), the
+ * forward's inputs and the rstds it left,
+ *   dq, dk in dtype, laid out by dq_stride and dk_stride (token rows, or views of
+ *       the projection's gradient; heads must not overlap)
+ *   dweight [2][d] float32: q_weight's, then k_weight's
+ * Sums over rows are float32 in a fixed order: the same call gives the same bits.
+ * dq may be q's buffer with q's strides (dk k's); no other output may alias an
+ * input.  Pointers but position, inv_freq and the rstds 16-byte aligned. */
+kdn_status kdn_qk_norm_rotary_backward(const kdn_rotary_desc *d, const void *dq_out,
+                                       const void *dk_out, const void *q, const void *k,
+                                       const float *q_weight, const float *k_weight,
+                                       const int32_t *position, const float *inv_freq,
+                                       const float *q_rstd, const float *k_rstd, void *dq,
+                                       void *dk, float *dweight, void *ws, size_t ws_bytes,
+                                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,6 +34,10 @@ Functions (same names as the C entry points):
   gated_delta_step(q, k, v, g, beta, S, slot=None) -> o   (one token, S in place)
   gated_delta_backward(q, k, v, g, beta, dO, S0=None, dS_T=None, cu_seqlens=None) -> dict of
                  gradients (dq, dk, dv, dg, dbeta in q's dtype, dS0 float32)
+  qk_norm_rotary(q, k, q_weight, k_weight, position, inv_freq) -> (q', k', q_rstd, k_rstd)
+                 (head norm, rotation by position, token rows to head rows)
+  qk_norm_rotary_backward(dq', dk', q, k, q_weight, k_weight, position, inv_freq, q_rstd,
+                          k_rstd) -> (dq, dk, dq_weight, dk_weight)
 """
 from __future__ import annotations
 
@@ -67,6 +71,8 @@ EXPORTS = (
     "kdn_gated_scan", "kdn_gated_scan_backward", "kdn_gated_scan_step",
     "kdn_gated_delta_workspace_bytes", "kdn_gated_delta", "kdn_gated_delta_step",
     "kdn_gated_delta_backward_workspace_bytes", "kdn_gated_delta_backward",
+    "kdn_qk_norm_rotary", "kdn_qk_norm_rotary_backward_workspace_bytes",
+    "kdn_qk_norm_rotary_backward",
 )
 
 
@@ -102,6 +108,13 @@ class KdnScanDesc(ctypes.Structure):
 class KdnDeltaDesc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "Hk", "T", "d_k", "d_v", "dtype",
                                                "gate_dtype")] + [("scale", ctypes.c_float)])
+
+
+class KdnRotaryDesc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "Hk", "d", "rot", "dtype",
+                                               "interleaved")] + [("eps", ctypes.c_float)] +
+                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "dq_stride",
+                                                   "dk_stride")])
 
 
 class KdnError(RuntimeError):
@@ -192,6 +205,11 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_gated_delta_backward_workspace_bytes.restype = S
     lib.kdn_gated_delta_backward.argtypes = [E] + [P] * 16 + [S, P]
     lib.kdn_gated_delta_step.argtypes = [E] + [P] * 7 + [ctypes.c_int32, P, P]
+    R = ctypes.POINTER(KdnRotaryDesc)
+    lib.kdn_qk_norm_rotary.argtypes = [R] + [P] * 11
+    lib.kdn_qk_norm_rotary_backward_workspace_bytes.argtypes = [R]
+    lib.kdn_qk_norm_rotary_backward_workspace_bytes.restype = S
+    lib.kdn_qk_norm_rotary_backward.argtypes = [R] + [P] * 14 + [S, P]
     _lib = lib
     return lib
 
@@ -1116,3 +1134,95 @@ def gated_delta_step(q, k, v, g, beta, S, slot=None, scale=None, out=None):
             v.data_ptr(), g.data_ptr(), beta.data_ptr(), S.data_ptr(), _ptr(slot), n_slots,
             o.data_ptr())
     return o
+
+
+def _rows_view(name, x, dev):
+    """A view of token rows [B,T,H,d]: on `dev`, columns contiguous."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise KdnError(f"{name} must be on a GPU (no CPU path exists)")
+    if x.dim() != 4 or (x.stride(3) != 1 and x.shape[3] > 1):
+        raise ValueError(f"{name} must be [B,T,H,d] with contiguous columns")
+    if dev is not None and x.device != dev:
+        raise ValueError(f"{name} is on {x.device}, the other tensors are on {dev}")
+    return x.device
+
+
+def _row_strides(x):
+    """Batch, token and head strides of a view of token rows; those of single entries, which
+    no address depends on, as 0."""
+    s = x.stride()
+    return (ctypes.c_int64 * 3)(*(s[i] if x.shape[i] > 1 else 0 for i in range(3)))
+
+
+def _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved):
+    if k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError("q and k must agree in all but their heads, and in dtype")
+    B, T, H, d = q.shape
+    _shaped("q_weight", q_weight, torch.float32, (d,))
+    _shaped("k_weight", k_weight, torch.float32, (d,))
+    if (position is None) != (inv_freq is None):
+        raise ValueError("position and inv_freq go together")
+    _shaped("position", position, torch.int32, (B, T))
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _shaped("inv_freq", inv_freq, torch.float32, (rot // 2,))
+    return KdnRotaryDesc(*_int32(B, T, H, k.shape[2], d, rot), _dtype_code(q.dtype),
+                         int(interleaved), eps, _row_strides(q), _row_strides(k))
+
+
+def qk_norm_rotary(q, k, q_weight, k_weight, position, inv_freq, eps=1e-6, interleaved=False):
+    """RMS norm of every head of queries and keys and the rotation by position, token rows
+    to the head rows that forward and gated_delta read.  q [B,T,H,d] and k [B,T,Hk,d]
+    float32 or bfloat16, views with contiguous columns (slices of a projection's rows:
+    strides multiples of 8); q_weight, k_weight float32 [d]; position int32 [B,T];
+    inv_freq float32 [rot / 2]: columns i and i + rot / 2 (interleaved: 2 i and 2 i + 1)
+    are turned by position * inv_freq[i], the columns behind rot are not.  position and
+    inv_freq None: no rotation.  Returns (q' [B,H,T,d], k' [B,Hk,T,d], and the inverse
+    roots q_rstd [B,H,T], k_rstd [B,Hk,T] float32)."""
+    dev = _tensors(("q_weight", q_weight), ("k_weight", k_weight), ("position", position),
+                   ("inv_freq", inv_freq))
+    dev = _rows_view("k", k, _rows_view("q", q, dev))
+    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved)
+    out = [_empty((n.B, h, n.T, n.d), q.dtype, dev) for h in (n.H, n.Hk)]
+    rstd = [_empty((n.B, h, n.T), torch.float32, dev) for h in (n.H, n.Hk)]
+    _launch("kdn_qk_norm_rotary", dev, ctypes.byref(n), q.data_ptr(), k.data_ptr(),
+            q_weight.data_ptr(), k_weight.data_ptr(), _ptr(position), _ptr(inv_freq),
+            out[0].data_ptr(), out[1].data_ptr(), rstd[0].data_ptr(), rstd[1].data_ptr())
+    return (*out, *rstd)
+
+
+def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, position, inv_freq, q_rstd,
+                            k_rstd, interleaved=False, out=None):
+    """Gradient of qk_norm_rotary from those of its first two outputs (dq_out [B,H,T,d],
+    dk_out [B,Hk,T,d], in q's dtype), its inputs and the rstds it returned.  Returns (dq
+    [B,T,H,d], dk [B,T,Hk,d] in q's dtype, dq_weight, dk_weight float32 [d]).  out:
+    optional (dq, dk) to write, views as q and k may be (slices of the projection's
+    gradient; q and k themselves are allowed)."""
+    dev = _tensors(("dq_out", dq_out), ("dk_out", dk_out), ("q_weight", q_weight),
+                   ("k_weight", k_weight), ("position", position), ("inv_freq", inv_freq),
+                   ("q_rstd", q_rstd), ("k_rstd", k_rstd))
+    _rows_view("k", k, _rows_view("q", q, dev))
+    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, 0.0, interleaved)
+    for name, x, r, h in (("dq_out", dq_out, q_rstd, n.H), ("dk_out", dk_out, k_rstd, n.Hk)):
+        _shaped(name, x, q.dtype, (n.B, h, n.T, n.d))
+        _shaped(name[1] + "_rstd", r, torch.float32, (n.B, h, n.T))
+    if out is None:
+        dq, dk = (_empty(tuple(x.shape), q.dtype, dev) for x in (q, k))
+    else:
+        dq, dk = out
+        for name, x, like in (("dq", dq, q), ("dk", dk, k)):
+            _rows_view(name, x, dev)
+            _shaped(name, x, q.dtype, like.shape)
+    n.dq_stride, n.dk_stride = _row_strides(dq), _row_strides(dk)
+    dw = _empty((2, n.d), torch.float32, dev)
+    need = load_library().kdn_qk_norm_rotary_backward_workspace_bytes(ctypes.byref(n))
+    ws = _empty((max(need, 16),), torch.uint8, dev)
+    _launch("kdn_qk_norm_rotary_backward", dev, ctypes.byref(n), dq_out.data_ptr(),
+            dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+            k_weight.data_ptr(), _ptr(position), _ptr(inv_freq), q_rstd.data_ptr(),
+            k_rstd.data_ptr(), dq.data_ptr(), dk.data_ptr(), dw.data_ptr(), ws.data_ptr(),
+            ws.numel())
+    return dq, dk, dw[0], dw[1]

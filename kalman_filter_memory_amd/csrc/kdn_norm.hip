@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "kdn.h"
+#include "kdn_norm.h"
 #include "kdn_quant.h"
 
 namespace {
@@ -423,6 +424,13 @@ template <typename Ex, typename Er> void bwd_width(const BwdNormArgs& a, hipStre
 }
 
 }  // namespace
+
+namespace kdn {
+hipError_t launch_column_sums(int n, int d, const float* rows, float* out, hipStream_t st) {
+    dw_kernel<<<(d + 31) / 32, 1024, 0, st>>>(n, d, rows, out);
+    return hipGetLastError();
+}
+}  // namespace kdn
 
 extern "C" {
 

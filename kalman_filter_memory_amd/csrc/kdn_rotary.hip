@@ -1,0 +1,363 @@
+// kdn_rotary.hip -- what stands between a projection and a recurrence over heads: the RMS
+// norm of every head of queries and keys, the rotation by position, and token rows to head
+// rows, in one pass; and its backward.
+//
+//   n = x r w,  r = (mean x^2 + eps)^(-1/2)         per head row of d columns
+//   y = n with the pairs of its first `rot` columns turned by position inv_freq_i:
+//   (a, b) -> (a cos - b sin, b cos + a sin), the pair (i, i + rot / 2) or (2 i, 2 i + 1)
+// Backward, with dn the gradient turned back and xhat = x r:
+//   dx = r (dn w - xhat mean(dn w xhat)),   dw = sum of dn xhat over tokens and heads
+//
+// Bound by HBM: a row is read once and written once.  The angles' products are taken in 64
+// bits and reduced to a turn there (a float32 product would be off by 2^-24 of the position),
+// once per token for all heads, by the workgroup that holds those tokens.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/kdn.h"
+#include "kdn_device.h"
+#include "kdn_norm.h"
+
+namespace kdn {
+namespace {
+
+constexpr int kRotThreads = 256, kMaxTile = 8, kMaxRowD = 256;
+constexpr int kMaxBackwardGroups = 1024;
+
+struct Side {  // of queries, or of keys
+    const void* x;
+    const float* w;
+    int64_t sb, st, sh;  // of x (backward: of dx too, below), in elements
+    int heads;
+    void* y;  // [B, heads, T, d]
+    float* rstd;
+};
+struct RotaryArgs {
+    Side side[2];
+    const int32_t* position;
+    const float* inv_freq;
+    int B, T, d, rot, tile, tiles;  // tile: tokens a workgroup takes at once (a power of two)
+    float eps;
+    // backward
+    const void* dy[2];
+    void* dx[2];
+    int64_t db[2], dt[2], dh[2];
+    float* part;  // [workgroups][2][d]
+};
+
+// eight elements to memory
+template <typename E> __device__ __forceinline__ void put8(E* p, const float (&f)[8]) {
+    if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<u32x4*>(p) =
+            u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+    } else {
+        reinterpret_cast<floatx4*>(p)[0] = floatx4{f[0], f[1], f[2], f[3]};
+        reinterpret_cast<floatx4*>(p)[1] = floatx4{f[4], f[5], f[6], f[7]};
+    }
+}
+
+// cos and sin of the tile's tokens: cs[token][0 .. rot / 2) and [rot / 2 .. rot)
+__device__ __forceinline__ void angles(const RotaryArgs& a, int first, int count, float* cs) {
+    const int half = a.rot >> 1;
+    for (int i = threadIdx.x; i < count * half; i += kRotThreads) {
+        const int t = i / half, p = i - t * half;
+        const double turn = double(a.position[first + t]) * double(a.inv_freq[p]) * 0.15915494309189533577;
+        float s, c;
+        sincospif(2.f * float(turn - rint(turn)), &s, &c);
+        cs[t * a.rot + p] = c;
+        cs[t * a.rot + half + p] = s;
+    }
+}
+
+// The row's columns c .. c + 7, turned (BACK: turned back): f holds them, g those of the
+// lane that holds the other halves of the pairs (halves only).
+template <bool NEIGHBOURS, bool BACK>
+__device__ __forceinline__ void turn(float (&f)[8], const float (&g)[8], const float* cs, int c, int rot) {
+    const int half = rot >> 1;
+    if constexpr (NEIGHBOURS) {
+        const floatx4 co = *reinterpret_cast<const floatx4*>(cs + (c >> 1));
+        const floatx4 si = *reinterpret_cast<const floatx4*>(cs + half + (c >> 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float s = BACK ? -si[i] : si[i], p = f[2 * i], q = f[2 * i + 1];
+            f[2 * i] = p * co[i] - q * s;
+            f[2 * i + 1] = q * co[i] + p * s;
+        }
+    } else {
+        const bool first = c < half;
+        const float* p = cs + (first ? c : c - half);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const floatx4 co = reinterpret_cast<const floatx4*>(p)[v];
+            const floatx4 si = *reinterpret_cast<const floatx4*>(p + half + 4 * v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = first != BACK ? -si[i] : si[i];
+                f[4 * v + i] = f[4 * v + i] * co[i] + g[4 * v + i] * s;
+            }
+        }
+    }
+}
+
+// x of the lane `from` of this group of LPR
+template <int LPR> __device__ __forceinline__ void from_lane(const float (&x)[8], float (&y)[8], int from) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], from, LPR);
+}
+
+// LPR lanes hold a row, eight columns each; consecutive groups take consecutive tokens of
+// one head, whose output rows are neighbours.
+template <typename E, int LPR, bool NEIGHBOURS>
+__global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotaryArgs a) {
+    __shared__ __align__(16) float cs[kMaxTile * kMaxRowD];
+    constexpr int GROUPS = kRotThreads / LPR;
+    const int64_t n = int64_t(a.B) * a.T;
+    const int64_t first = int64_t(blockIdx.x) * a.tile;
+    const int count = int(std::min<int64_t>(a.tile, n - first));
+    angles(a, int(first), count, cs);
+    __syncthreads();
+    const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, c = 8 * l;
+    const bool in = c < a.d, turned = c < a.rot;
+    const int other = c < (a.rot >> 1) ? l + (a.rot >> 4) : l - (a.rot >> 4);
+    const int shift = __builtin_ctz(a.tile);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const Side s = a.side[k];
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0.f;
+        if (in) load_vec<float, 8>(s.w + c, w);
+        const int rows = s.heads << shift;
+        for (int r = grp; r < rows; r += GROUPS) {
+            const int t = r & (a.tile - 1), h = r >> shift;
+            if (t >= count) continue;  // (a whole group)
+            const uint32_t token = uint32_t(first) + uint32_t(t), b = token / uint32_t(a.T), tt = token - b * uint32_t(a.T);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+            if (in)
+                load_vec<E, 8>(static_cast<const E*>(s.x) + int64_t(b) * s.sb + int64_t(tt) * s.st + int64_t(h) * s.sh + c, x);
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            ss = group_sum<LPR>(ss);
+            const float rstd = 1.f / sqrtf(ss / float(a.d) + a.eps);
+            float y[8], o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i] * rstd * w[i];
+            if (!NEIGHBOURS) from_lane<LPR>(y, o, other);
+            if (turned) turn<NEIGHBOURS, false>(y, o, cs + t * a.rot, c, a.rot);
+            const size_t row = (size_t(b) * s.heads + h) * a.T + tt;
+            if (in) put8<E>(static_cast<E*>(s.y) + row * a.d + c, y);
+            if (s.rstd != nullptr && l == 0) s.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename E, int LPR, bool NEIGHBOURS>
+__global__ __launch_bounds__(kRotThreads) void rotary_backward_kernel(RotaryArgs a) {
+    __shared__ __align__(16) float cs[kMaxTile * kMaxRowD];
+    constexpr int GROUPS = kRotThreads / LPR;
+    const int64_t n = int64_t(a.B) * a.T;
+    const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR, c = 8 * l;
+    const bool in = c < a.d, turned = c < a.rot;
+    const int other = c < (a.rot >> 1) ? l + (a.rot >> 4) : l - (a.rot >> 4);
+    const int shift = __builtin_ctz(a.tile);
+    const float inv_d = 1.f / float(a.d);
+    float dw[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+        const int64_t first = int64_t(tile) * a.tile;
+        const int count = int(std::min<int64_t>(a.tile, n - first));
+        __syncthreads();  // the angles of the tile before are done with
+        angles(a, int(first), count, cs);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Side s = a.side[k];
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0.f;
+            if (in) load_vec<float, 8>(s.w + c, w);
+            const int rows = s.heads << shift;
+            for (int r = grp; r < rows; r += GROUPS) {
+                const int t = r & (a.tile - 1), h = r >> shift;
+                if (t >= count) continue;
+                const uint32_t token = uint32_t(first) + uint32_t(t), b = token / uint32_t(a.T), tt = token - b * uint32_t(a.T);
+                const size_t row = (size_t(b) * s.heads + h) * a.T + tt;
+                float x[8], f[8], o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = f[i] = 0.f;
+                if (in) {
+                    load_vec<E, 8>(static_cast<const E*>(a.dy[k]) + row * a.d + c, f);
+                    load_vec<E, 8>(static_cast<const E*>(s.x) + int64_t(b) * s.sb + int64_t(tt) * s.st + int64_t(h) * s.sh + c, x);
+                }
+                const float rstd = s.rstd[row];
+                if (!NEIGHBOURS) from_lane<LPR>(f, o, other);
+                if (turned) turn<NEIGHBOURS, true>(f, o, cs + t * a.rot, c, a.rot);
+                float along = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] *= rstd;
+                    dw[k][i] = fmaf(f[i], x[i], dw[k][i]);
+                    f[i] *= w[i];
+                    along = fmaf(f[i], x[i], along);
+                }
+                along = group_sum<LPR>(along) * inv_d;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = rstd * (f[i] - x[i] * along);
+                if (in)
+                    put8<E>(static_cast<E*>(a.dx[k]) + int64_t(b) * a.db[k] + int64_t(tt) * a.dt[k] + int64_t(h) * a.dh[k] + c, f);
+            }
+        }
+    }
+    // the groups' sums meet, one of the two weights after the other
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        __syncthreads();
+        put8<float>(cs + threadIdx.x * 8, dw[k]);  // [group][8 LPR columns]
+        __syncthreads();
+        for (int j = threadIdx.x; j < a.d; j += kRotThreads) {
+            float sum = 0.f;
+            for (int i = 0; i < GROUPS; ++i) sum += cs[i * 8 * LPR + j];
+            a.part[(size_t(blockIdx.x) * 2 + k) * a.d + j] = sum;
+        }
+    }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+kdn_status check(const kdn_rotary_desc* d) {
+    if (!d) return KDN_ERR_NULL;
+    if (d->B < 0 || d->T < 0 || d->H < 0 || d->Hk < 0 || d->d < 0 || d->rot < 0 || d->rot > d->d) return KDN_ERR_SHAPE;
+    if (!(d->eps >= 0.f) || d->eps - d->eps != 0.f) return KDN_ERR_SHAPE;
+    if (d->dtype != KDN_F32 && d->dtype != KDN_BF16) return KDN_ERR_UNSUPPORTED;
+    if (d->d == 0 || d->d % 8 != 0 || d->d > kMaxRowD || d->rot % 16 != 0) return KDN_ERR_UNSUPPORTED;
+    if (int64_t(d->B) * d->T >= (int64_t(1) << 26) || d->H > (1 << 16) || d->Hk > (1 << 16)) return KDN_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        if (d->q_stride[i] % 8 != 0 || d->k_stride[i] % 8 != 0 || d->dq_stride[i] % 8 != 0 || d->dk_stride[i] % 8 != 0)
+            return KDN_ERR_ALIGN;
+    return KDN_OK;
+}
+
+// Tokens a workgroup takes at once: one where that leaves few workgroups.
+int tile_of(int64_t tokens) { return tokens >= 4096 ? kMaxTile : 1; }
+
+unsigned backward_groups(const kdn_rotary_desc* d) {
+    const int64_t n = int64_t(d->B) * d->T, tile = tile_of(n);
+    return unsigned(std::min<int64_t>((n + tile - 1) / tile, kMaxBackwardGroups));
+}
+
+RotaryArgs args_of(const kdn_rotary_desc* d, const void* q, const void* k, const float* q_weight, const float* k_weight,
+                   const int32_t* position, const float* inv_freq) {
+    RotaryArgs a{};
+    a.side[0] = Side{q, q_weight, d->q_stride[0], d->q_stride[1], d->q_stride[2], d->H, nullptr, nullptr};
+    a.side[1] = Side{k, k_weight, d->k_stride[0], d->k_stride[1], d->k_stride[2], d->Hk, nullptr, nullptr};
+    a.position = position;
+    a.inv_freq = inv_freq;
+    a.B = d->B;
+    a.T = d->T;
+    a.d = d->d;
+    a.rot = d->rot;
+    a.eps = d->eps;
+    const int64_t n = int64_t(d->B) * d->T;
+    a.tile = tile_of(n);
+    a.tiles = int((n + a.tile - 1) / a.tile);
+    return a;
+}
+
+template <typename E, int LPR> void launch_lpr(const RotaryArgs& a, bool neighbours, unsigned groups, bool bwd, hipStream_t st) {
+    if (bwd) {
+        if (neighbours) rotary_backward_kernel<E, LPR, true><<<groups, kRotThreads, 0, st>>>(a);
+        else rotary_backward_kernel<E, LPR, false><<<groups, kRotThreads, 0, st>>>(a);
+    } else {
+        if (neighbours) rotary_kernel<E, LPR, true><<<groups, kRotThreads, 0, st>>>(a);
+        else rotary_kernel<E, LPR, false><<<groups, kRotThreads, 0, st>>>(a);
+    }
+}
+template <typename E> void launch_e(const RotaryArgs& a, bool neighbours, unsigned groups, bool bwd, hipStream_t st) {
+    if (a.d <= 32) launch_lpr<E, 4>(a, neighbours, groups, bwd, st);
+    else if (a.d <= 64) launch_lpr<E, 8>(a, neighbours, groups, bwd, st);
+    else if (a.d <= 128) launch_lpr<E, 16>(a, neighbours, groups, bwd, st);
+    else launch_lpr<E, 32>(a, neighbours, groups, bwd, st);
+}
+hipError_t launch(const RotaryArgs& a, const kdn_rotary_desc* d, unsigned groups, bool bwd, hipStream_t st) {
+    if (d->dtype == KDN_BF16) launch_e<bf16_t>(a, d->interleaved != 0, groups, bwd, st);
+    else launch_e<float>(a, d->interleaved != 0, groups, bwd, st);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace kdn
+
+extern "C" {
+
+kdn_status kdn_qk_norm_rotary(const kdn_rotary_desc* d, const void* q, const void* k, const float* q_weight,
+                              const float* k_weight, const int32_t* position, const float* inv_freq, void* q_out, void* k_out,
+                              float* q_rstd, float* k_rstd, void* stream) {
+    using namespace kdn;
+    const kdn_status c = check(d);
+    if (c != KDN_OK) return c;
+    if (d->B == 0 || d->T == 0 || (d->H == 0 && d->Hk == 0)) return KDN_OK;
+    for (const void* p : {q, k, (const void*)q_weight, (const void*)k_weight, (const void*)q_out, (const void*)k_out})
+        if (!aligned16(p)) return KDN_ERR_ALIGN;
+    if ((d->H > 0 && (!q || !q_weight || !q_out)) || (d->Hk > 0 && (!k || !k_weight || !k_out))) return KDN_ERR_NULL;
+    if (d->rot > 0 && (!position || !inv_freq)) return KDN_ERR_NULL;
+    RotaryArgs a = args_of(d, q, k, q_weight, k_weight, position, inv_freq);
+    a.side[0].y = q_out;
+    a.side[1].y = k_out;
+    a.side[0].rstd = q_rstd;
+    a.side[1].rstd = k_rstd;
+    return launch(a, d, unsigned(a.tiles), false, static_cast<hipStream_t>(stream)) == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+}
+
+size_t kdn_qk_norm_rotary_backward_workspace_bytes(const kdn_rotary_desc* d) {
+    using namespace kdn;
+    if (check(d) != KDN_OK) return 0;
+    return std::max<size_t>(size_t(backward_groups(d)) * 2 * d->d * 4, 16);
+}
+
+kdn_status kdn_qk_norm_rotary_backward(const kdn_rotary_desc* d, const void* dq_out, const void* dk_out, const void* q,
+                                       const void* k, const float* q_weight, const float* k_weight, const int32_t* position,
+                                       const float* inv_freq, const float* q_rstd, const float* k_rstd, void* dq, void* dk,
+                                       float* dweight, void* ws, size_t ws_bytes, void* stream) {
+    using namespace kdn;
+    const kdn_status c = check(d);
+    if (c != KDN_OK) return c;
+    for (const void* p : {dq_out, dk_out, q, k, (const void*)q_weight, (const void*)k_weight, (const void*)dq,
+                          (const void*)dk, (const void*)dweight, (const void*)ws})
+        if (!aligned16(p)) return KDN_ERR_ALIGN;
+    if (!dweight) return KDN_ERR_NULL;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool none = d->B == 0 || d->T == 0;  // dweight is then zero
+    if (!none) {
+        if ((d->H > 0 && (!q || !q_weight || !dq_out || !dq || !q_rstd)) ||
+            (d->Hk > 0 && (!k || !k_weight || !dk_out || !dk || !k_rstd)) || !ws)
+            return KDN_ERR_NULL;
+        if (d->rot > 0 && (!position || !inv_freq)) return KDN_ERR_NULL;
+        if (ws_bytes < kdn_qk_norm_rotary_backward_workspace_bytes(d)) return KDN_ERR_WORKSPACE;
+        RotaryArgs a = args_of(d, q, k, q_weight, k_weight, position, inv_freq);
+        a.side[0].rstd = const_cast<float*>(q_rstd);
+        a.side[1].rstd = const_cast<float*>(k_rstd);
+        a.dy[0] = dq_out;
+        a.dy[1] = dk_out;
+        a.dx[0] = dq;
+        a.dx[1] = dk;
+        for (int i = 0; i < 2; ++i) {
+            const int64_t* s = i == 0 ? d->dq_stride : d->dk_stride;
+            a.db[i] = s[0];
+            a.dt[i] = s[1];
+            a.dh[i] = s[2];
+        }
+        a.part = static_cast<float*>(ws);
+        if (launch(a, d, backward_groups(d), true, st) != hipSuccess) return KDN_ERR_HIP;
+    }
+    return launch_column_sums(none ? 0 : int(backward_groups(d)), 2 * d->d, static_cast<const float*>(ws), dweight, st) ==
+                   hipSuccess
+               ? KDN_OK
+               : KDN_ERR_HIP;
+}
+
+}  // extern "C"
