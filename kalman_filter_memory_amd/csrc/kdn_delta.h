@@ -28,6 +28,24 @@ template <int N> struct Planes {
     bf16x8 p[N];
 };
 
+// x minus the first (second) of two bfloat16, exactly, in one instruction: a product of
+// the pair with (-1, 0) or (0, -1).  The constants come from registers: as an immediate,
+// -1 would be taken in the other half.
+__device__ __forceinline__ float less_pair(float x, uint32_t w, uint32_t minus_one) {
+    typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(pair_t, w), __builtin_bit_cast(pair_t, minus_one), x, false);
+}
+__device__ __forceinline__ float less_first(float x, uint32_t w) {
+    uint32_t c;
+    asm("s_mov_b32 %0, 0xbf80" : "=s"(c));
+    return less_pair(x, w, c);
+}
+__device__ __forceinline__ float less_second(float x, uint32_t w) {
+    uint32_t c;
+    asm("s_mov_b32 %0, 0xbf800000" : "=s"(c));
+    return less_pair(x, w, c);
+}
+
 // eight floats as the sum of N planes, largest first (each the rounding of what the ones
 // before it left)
 template <int N> __device__ __forceinline__ Planes<N> split8(const float (&f)[8]) {
@@ -42,8 +60,8 @@ template <int N> __device__ __forceinline__ Planes<N> split8(const float (&f)[8]
         for (int i = 0; i < 4; ++i) {
             w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
             if (n + 1 < N) {
-                x[2 * i] -= __uint_as_float(w[i] << 16);
-                x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+                x[2 * i] = less_first(x[2 * i], w[i]);
+                x[2 * i + 1] = less_second(x[2 * i + 1], w[i]);
             }
         }
         r.p[n] = __builtin_bit_cast(bf16x8, w);
@@ -59,10 +77,10 @@ template <int N> __device__ __forceinline__ void split4(const float (&f)[4], uin
         const uint32_t a = pack_bf16(x[0], x[1]), b = pack_bf16(x[2], x[3]);
         r[n] = make_uint2(a, b);
         if (n + 1 < N) {
-            x[0] -= __uint_as_float(a << 16);
-            x[1] -= __uint_as_float(a & 0xffff0000u);
-            x[2] -= __uint_as_float(b << 16);
-            x[3] -= __uint_as_float(b & 0xffff0000u);
+            x[0] = less_first(x[0], a);
+            x[1] = less_second(x[1], a);
+            x[2] = less_first(x[2], b);
+            x[3] = less_second(x[3], b);
         }
     }
 }
@@ -185,7 +203,8 @@ template <int S> __device__ __forceinline__ float row_bcast(float x) {
 template <int S> __device__ __forceinline__ void substitute(const float (&a)[16], float (&x)[8]) {
     if constexpr (S < 15) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = fmaf(-a[S], row_bcast<S>(x[j]), x[j]);
+        for (int j = 0; j < 8; ++j)
+            if (j <= S) x[j] = fmaf(-a[S], row_bcast<S>(x[j]), x[j]);  // (columns behind S hold 0 in row S)
         substitute<S + 1>(a, x);
     }
 }
@@ -244,6 +263,20 @@ __device__ __forceinline__ void invert(const float* A, float* tmp, bf16_t* out, 
 #pragma unroll
     for (int n = 0; n < 3; ++n)
         *reinterpret_cast<uint2*>(out + n * C * C + square_at(row, col >> 3) + (col & 7)) = p[n];
+}
+
+// 16 bytes per lane from base + off straight into LDS, lane l's to lds + 16 l.  Inline
+// assembly because the compiler would wait for the copy before any later LDS read; the
+// waits are copies_done's, by the wave that copies (m0 needs one wait state).
+__device__ __forceinline__ void copy_to_lds(const void* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(lds) : "memory");
+}
+template <int LATER> __device__ __forceinline__ void copies_done() {  // but the last LATER
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LATER) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    typedef __attribute__((address_space(3))) const char lds_char;
+    return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(reinterpret_cast<uintptr_t>((lds_char*)p))));
 }
 
 // ------------------------------------------------------------- a chunk's LDS, and helpers

@@ -270,6 +270,284 @@ template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hi
     else forward_d<E, 128>(a, keep, st);
 }
 
+// ---------------------------------------------------------------------- bfloat16 inputs
+// The same recurrence with everything a chunk needs prepared further ahead, one barrier
+// per chunk and the rows copied straight into LDS.  While the recurrence is at chunk c,
+//   helper 3       copies chunk c + 4 (rows behind the sequence's last: that row again;
+//                  beta 0 keeps them out of the state)
+//   helper 2       sums the decays of chunk c + 3, and forms P of chunk c + 1
+//   helpers 0, 1   form the triangular system of chunk c + 2, and invert that of c + 1,
+//                  taking turns (a chunk stays with one of them)
+template <int DK, int DV, bool KEEP> struct AheadLds {
+    static constexpr int W = DV == 32 ? 2 : 4, COLS = 16 * W;
+    bf16_t k[5][C * DK];
+    bf16_t q[KEEP ? 1 : 5][KEEP ? 8 : C * DK];
+    bf16_t v[5][C * COLS];
+    bf16_t t[2][3 * C * C];
+    bf16_t p[KEEP ? 1 : 2][KEEP ? 8 : 2 * C * C];
+    float a[2][C * kLdA];
+    float tmp[2][32 * kLdT];
+    float gam[4][C], rest[4][C], beta[4][C];
+    LogSum G[4][C];
+};
+
+// 16-byte pieces of a row of v's columns, swapped in every second pair of rows, so that
+// the four rows of a transposing read meet every bank once
+template <int COLS> __device__ __forceinline__ int value_at(int row, int piece) {
+    return row * COLS + ((piece ^ (((row >> 1) & 1) << 1)) << 3);
+}
+
+// Copies a chunk's 32 rows of D columns (in the order of Rows<D>, or of value_at) with one
+// wave: rows are `stride` elements apart, the last of `rows` stands in for those behind it.
+template <int D, bool VALUES>
+__device__ __forceinline__ void copy_rows(const bf16_t* x, unsigned stride, int rows, uint32_t lds, int lane) {
+    constexpr int kPer = D / 8, kRows = 64 / kPer;  // pieces of a row, rows of a copy
+#pragma unroll
+    for (int i = 0; i < C / kRows; ++i) {
+        const int row = kRows * i + lane / kPer, at = lane % kPer;
+        // the piece that belongs at place `at` (both orders are their own inverses)
+        const int piece = ((VALUES ? value_at<D>(row, at) : Rows<D>::at(row, at)) - row * D) >> 3;
+        copy_to_lds(x, unsigned(min(row, rows - 1)) * stride * 2u + unsigned(piece) * 16u, lds + 1024u * i);
+    }
+}
+
+template <int DK, int DV, bool KEEP>
+__global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
+    using Lds = AheadLds<DK, DV, KEEP>;
+    constexpr int W = Lds::W, COLS = Lds::COLS;
+    using Cf = Cfg<bf16_t, DK, W>;
+    constexpr int KT = Cf::KT, KS = Cf::KS;
+    __shared__ __align__(16) Lds L;
+
+    constexpr unsigned slices = DV / COLS;
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
+    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int nc = (sq.len + C - 1) / C;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int col0 = slice * COLS;
+    const size_t state = (size_t(b) * a.H + h) * size_t(DV) * DK;
+
+    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += 64 * (W + 4))
+        reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
+    if constexpr (!KEEP)
+        for (unsigned i = threadIdx.x; i < 2 * 2 * C * C / 8; i += 64 * (W + 4))
+            reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
+
+    if (wave >= W) {
+        const int hw = wave - W;
+        if (hw == 3) {
+            const bf16_t* q = static_cast<const bf16_t*>(a.q) + sq.rq * DK;
+            const bf16_t* k = static_cast<const bf16_t*>(a.k) + sq.rq * DK;
+            const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + col0;
+            constexpr int kCopies = C * DK / 512 * (KEEP ? 1 : 2) + C * COLS / 512;
+            const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), lv = lds_address(L.v);
+            auto copy = [&](int c, int s) {
+                const int rows = sq.len - c * C;
+                copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
+                if constexpr (!KEEP) copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
+                copy_rows<COLS, true>(v + size_t(c) * (C * DV), DV, rows, lv + s * (C * COLS * 2), lane);
+            };
+            if (nc > 0) copy(0, 0);
+            if (nc > 1) copy(1, 1);
+            copies_done<0>();
+            sync_lds();
+            int s = 2;
+            for (int c = -2; c < nc; ++c) {
+                if (c + 4 < nc) {
+                    copy(c + 4, s);
+                    copies_done<kCopies>();
+                } else {
+                    copies_done<0>();
+                }
+                s = s == 4 ? 0 : s + 1;
+                sync_lds();
+            }
+        } else if (hw == 2) {
+            float g = 0.f, be = 0.f;
+            auto gates = [&](int c) {
+                const int t = c * C + (lane & 31);
+                g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
+                be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
+            };
+            auto sums = [&](int c) {
+                const int s = c & 3;
+                const LogSum G = log_sums<C>(g, lane);
+                const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
+                if (lane < C) {
+                    L.G[s][lane] = G;
+                    L.gam[s][lane] = decay_of(G);
+                    L.rest[s][lane] = decay_between(last, G);
+                    L.beta[s][lane] = be;
+                }
+            };
+            gates(0);
+            sums(0);
+            gates(1);
+            sync_lds();
+            int s = 4;  // where chunk c + 1 is
+            for (int c = -2; c < nc; ++c) {
+                if (c + 3 < nc) {
+                    sums(c + 3);
+                    gates(c + 4);
+                }
+                if constexpr (!KEEP)
+                    if (c >= -1 && c + 1 < nc)
+                        readout_of<Cf, false, 2>(L.q[s], L.k[s], L.G[(c + 1) & 3], a.scale, L.p[(c + 1) & 1], lane);
+                s = s == 4 ? 0 : s + 1;
+                sync_lds();
+            }
+        } else {
+            sync_lds();
+            int s = 0;  // where chunk c + 2 is
+            for (int c = -2; c < nc; ++c) {
+                if ((c & 1) == hw) {
+                    if (c + 2 < nc) system_of<Cf, false>(L.k[s], L.G[(c + 2) & 3], L.beta[(c + 2) & 3], L.a[hw], lane);
+                } else if (c >= -1 && c + 1 < nc) {
+                    invert<false>(L.a[hw], L.tmp[hw], L.t[(c + 1) & 1], lane);
+                }
+                s = s == 4 ? 0 : s + 1;
+                sync_lds();
+            }
+        }
+        return;
+    }
+
+    // --------------------------------------------------------------------- recurrence
+    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
+    floatx4 st[KT];
+    if (a.S0 != nullptr) {
+        load_state<KS>(st, a.S0 + state, col, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    const size_t groups = KEEP ? group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) : 0;
+    // this lane's outputs of a chunk: rows 8 g + 0..7 of its column
+    bf16_t* out = static_cast<bf16_t*>(KEEP ? a.keep_E : a.o) + (sq.rv + 8 * g) * DV + col;
+    sync_lds();
+    sync_lds();
+    sync_lds();
+    // What is left of a chunk when the state has gone on: o = scale gamma Q S + P U (or E)
+    floatx4 left[2];
+    Planes<2> lu, lp[2];
+    auto results = [&](float (&f)[8]) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const floatx4 o = KEEP ? left[x] : product<1>(lp[x], lu, left[x]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * x + e] = o[e];
+        }
+    };
+    Planes<1> kf[2][KS], qf[2][KS];
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
+                if constexpr (!KEEP) qf[x][j] = row_frag<Cf>(L.q[s], x, j, lane);
+            }
+    };
+    int s = 0;
+    if (nc > 0) fetch(0);
+    for (int c = 0; c < nc; ++c) {
+        const int sg = c & 3;
+        if constexpr (KEEP) {
+            if (c % a.group == 0)
+                keep_state<bf16_t, KS>(
+                    st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK, col, lane);
+        }
+        floatx4 ks[2], qs[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            const Planes<3> sp = state_planes<KT>(st, j);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ks[x] = product<2>(kf[x][j], sp, ks[x]);
+            if constexpr (!KEEP)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) qs[x] = product<1>(qf[x][j], sp, qs[x]);
+        }
+        if (c > 0) {  // the chunk before (a whole one)
+            float f[8];
+            results(f);
+            bf16_t* p = out + size_t(c - 1) * (C * DV);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e * DV] = f2bf(f[e]);
+        }
+        floatx4 gam[2], be[2], rest[2];
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t = 8 * g + 4 * x;
+            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
+            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[sg][t]);
+            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[sg][t]);
+            const short4x w = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * x + e] = bf2f(static_cast<bf16_t>(w[e])) - gam[x][e] * ks[x][e];
+        }
+        const Planes<3> rp = split8<3>(f);
+        floatx4 ee[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            ee[x] = product<2>(square_frag<3>(L.t[c & 1], x, lane), rp, floatx4{0.f, 0.f, 0.f, 0.f});
+        float u[8], ub[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                u[4 * x + e] = be[x][e] * ee[x][e];
+                ub[4 * x + e] = rest[x][e] * u[4 * x + e];
+                left[x][e] = KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
+            }
+        if constexpr (!KEEP) {
+            lu = split8<2>(u);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) lp[x] = square_frag<2>(L.p[c & 1], x, lane);
+        }
+        const Planes<3> up = split8<3>(ub);
+        const float last = L.gam[sg][C - 1];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const floatx4 w = {last * st[i][0], last * st[i][1], last * st[i][2], last * st[i][3]};
+            st[i] = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), up, w);
+        }
+        s = s == 4 ? 0 : s + 1;
+        if (c + 1 < nc) fetch(s);
+        sync_lds();
+    }
+    if (nc > 0) {
+        float f[8];
+        results(f);
+        bf16_t* p = out + size_t(nc - 1) * (C * DV);
+        const int rows = sq.len - (nc - 1) * C - 8 * g;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < rows) p[e * DV] = f2bf(f[e]);
+    }
+    if (a.S_T != nullptr) store_state<KS>(st, a.S_T + state, col, lane);
+}
+
+template <int DK, int DV> void ahead_go(const ForwardArgs& a, bool keep, hipStream_t st) {
+    constexpr int W = AheadLds<DK, DV, false>::W;
+    const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
+    if (keep) delta_ahead_kernel<DK, DV, true><<<n, 64 * (W + 4), 0, st>>>(a);
+    else delta_ahead_kernel<DK, DV, false><<<n, 64 * (W + 4), 0, st>>>(a);
+}
+template <int DK> void ahead_dv(const ForwardArgs& a, bool keep, hipStream_t st) {
+    if (a.dv == 32) ahead_go<DK, 32>(a, keep, st);
+    else if (a.dv == 64) ahead_go<DK, 64>(a, keep, st);
+    else ahead_go<DK, 128>(a, keep, st);
+}
+void forward_bf16(const ForwardArgs& a, int dk, bool keep, hipStream_t st) {
+    if (dk == 32) ahead_dv<32>(a, keep, st);
+    else if (dk == 64) ahead_dv<64>(a, keep, st);
+    else ahead_dv<128>(a, keep, st);
+}
+
 // ------------------------------------------------------------------------- one token
 // d_k / 4 lanes per row of S, four elements each; a workgroup owns one state, every wave
 // d_v / NW of its rows.  Bound by the state's 8 d_k d_v bytes.
@@ -379,7 +657,7 @@ kdn_status check(const kdn_delta_desc* d, bool one_token) {
 }
 
 hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st) {
-    if (dtype == KDN_BF16) forward_e<bf16_t>(a, dk, keep, st);
+    if (dtype == KDN_BF16) forward_bf16(a, dk, keep, st);
     else forward_e<float>(a, dk, keep, st);
     return hipGetLastError();
 }
