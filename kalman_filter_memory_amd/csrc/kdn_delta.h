@@ -110,6 +110,23 @@ __device__ __forceinline__ floatx4 product(const Planes<NA>& a, const Planes<NB>
     return c;
 }
 
+// the rounding of a pair of result tiles, as the operand of the next contraction
+__device__ __forceinline__ bf16x8 pack8(floatx4 a, floatx4 b) {
+    return __builtin_bit_cast(bf16x8, u32x4{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])});
+}
+
+// Minus the unit matrix for result tile h of a pair: minus_unit . pack8(a, b) + (a or b) is
+// what the rounding left, exactly, on the matrix unit instead of 8 vector instructions.
+__device__ __forceinline__ bf16x8 minus_unit(int lane, int h) {
+    u32x4 w = {0, 0, 0, 0};
+    const int m = lane & 15, i = (m & 3) + 4 * h;
+    if (m >> 2 == lane >> 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = i >> 1 == e ? ((i & 1) ? 0xbf800000u : 0x0000bf80u) : 0u;
+    }
+    return __builtin_bit_cast(bf16x8, w);
+}
+
 // ------------------------------------------------------------------ token rows in LDS
 // Rows of D elements (a plane), the 16-byte pieces of row t stored at piece ^ f(t): both
 // the row-wise fragments (pieces of 16 rows) and the transposing reads (4 pieces of 4
@@ -173,13 +190,33 @@ __device__ __forceinline__ double log2_decay(float g) {
     const double x = double(g) * 1.4426950408889634;
     return x < -160.0 ? -160.0 : x;
 }
-// inclusive sums over each N lanes of a wave
+// a double of another lane of the row of 16 (DPP control CTRL), 0 from outside it
+template <int CTRL> __device__ __forceinline__ double dpp_double(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), CTRL, 0xF, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), CTRL, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lane_double(double x, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(int(uint32_t(u)), l), hi = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), l);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+}
+// inclusive sums over each N lanes of a wave: rows of 16 by shifts, then the rows' totals
 template <int N> __device__ __forceinline__ LogSum log_sums(float g, int lane) {
+    static_assert(N == 32 || N == 64, "rows are joined for one or two pairs");
     double x = log2_decay(g);
-#pragma unroll
-    for (int d = 1; d < N; d <<= 1) {
-        const double y = __shfl_up(x, d, N);
-        x += (lane & (N - 1)) >= d ? y : 0.0;
+    x += dpp_double<0x111>(x);  // row_shr 1, 2, 4, 8
+    x += dpp_double<0x112>(x);
+    x += dpp_double<0x114>(x);
+    x += dpp_double<0x118>(x);
+    const int row = lane >> 4;
+    if constexpr (N == 32) {
+        const double a = lane_double(x, 15), b = lane_double(x, 47);
+        x += (row & 1) ? (row == 1 ? a : b) : 0.0;
+    } else {
+        const double a = lane_double(x, 15), b = a + lane_double(x, 31), c = b + lane_double(x, 47);
+        x += row == 0 ? 0.0 : row == 1 ? a : row == 2 ? b : c;
     }
     const float hi = float(x);
     return LogSum{hi, float(x - double(hi))};
@@ -337,24 +374,29 @@ template <typename E, int D, int THREADS> struct Stage {
     }
 };
 
-// k_t.k_s (or q_t.k_s) of a 16 x 16 block: rows r0 of x against columns c0 of y
-template <typename Cf, int LIM>
-__device__ __forceinline__ floatx4 dots(const bf16_t* x, int r0, const bf16_t* y, int c0, int lane) {
+// Blocks (0,0), (1,0) and (1,1) of 16 x 16 of x y^T (first index: x's rows), or with
+// UPPER (0,0), (0,1), (1,1)
+template <typename Cf, int LIM, bool UPPER>
+__device__ __forceinline__ void dots(const bf16_t* x, const bf16_t* y, floatx4 (&c)[3], int lane) {
     constexpr int NP = Cf::NP;
     using T = typename Cf::Tile;
     const int m = lane & 15, g = lane >> 4;
-    floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) c[i] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < Cf::KS; ++j) {
-        Planes<NP> a, b;
+        Planes<NP> a[2], b[2];
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            a.p[n] = T::row(x + n * C * Cf::DK, r0 + m, 4 * j + g);
-            b.p[n] = T::row(y + n * C * Cf::DK, c0 + m, 4 * j + g);
-        }
-        c = product<LIM>(a, b, c);
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[i].p[n] = T::row(x + n * C * Cf::DK, 16 * i + m, 4 * j + g);
+                b[i].p[n] = T::row(y + n * C * Cf::DK, 16 * i + m, 4 * j + g);
+            }
+        c[0] = product<LIM>(a[0], b[0], c[0]);
+        c[1] = UPPER ? product<LIM>(a[0], b[1], c[1]) : product<LIM>(a[1], b[0], c[1]);
+        c[2] = product<LIM>(a[1], b[1], c[2]);
     }
-    return c;
 }
 
 // The system's strictly lower triangle, A_ts = Gamma_ts k_t.k_s scaled by beta_s (its
@@ -363,12 +405,14 @@ __device__ __forceinline__ floatx4 dots(const bf16_t* x, int r0, const bf16_t* y
 template <typename Cf, bool REV>
 __device__ __forceinline__ void system_of(const bf16_t* k, const LogSum* G, const float* beta, float* A, int lane) {
     const int m = lane & 15, g = lane >> 4;
+    floatx4 all[3];
+    dots<Cf, 2, !REV>(k, k, all, lane);
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         const int bt = x == 0 ? 0 : 1, bs = x == 2 ? 1 : 0;  // blocks (0,0), (1,0), (1,1)
+        const floatx4 d = all[x];
         if constexpr (!REV) {
             // rows are s = 16 bs + 4 g + e, this lane's column is t
-            const floatx4 d = dots<Cf, 2>(k, 16 * bs, k, 16 * bt, lane);
             const int t = 16 * bt + m, s0 = 16 * bs + 4 * g;
             floatx4 v;
 #pragma unroll
@@ -377,7 +421,6 @@ __device__ __forceinline__ void system_of(const bf16_t* k, const LogSum* G, cons
             *reinterpret_cast<floatx4*>(A + t * kLdA + s0) = v;
         } else {
             // rows are t = 16 bt + 4 g + e, this lane's column is s
-            const floatx4 d = dots<Cf, 2>(k, 16 * bt, k, 16 * bs, lane);
             const int s = 16 * bs + m, t0 = 16 * bt + 4 * g;
             floatx4 v;
 #pragma unroll
@@ -394,20 +437,22 @@ template <typename Cf, bool TRANSPOSED, int NPL>
 __device__ __forceinline__ void readout_of(const bf16_t* q, const bf16_t* k, const LogSum* G, float scale, bf16_t* out,
                                            int lane) {
     const int m = lane & 15, g = lane >> 4;
+    floatx4 all[3];
+    if constexpr (TRANSPOSED) dots<Cf, NPL - 1, false>(q, k, all, lane);
+    else dots<Cf, NPL - 1, true>(k, q, all, lane);
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
         const int bt = x == 0 ? 0 : 1, bs = x == 2 ? 1 : 0;
+        const floatx4 d = all[x];
         float v[4];
         int row, col;
         if constexpr (!TRANSPOSED) {
-            const floatx4 d = dots<Cf, NPL - 1>(k, 16 * bs, q, 16 * bt, lane);
             const int t = 16 * bt + m, s0 = 16 * bs + 4 * g;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = s0 + e <= t ? scale * d[e] * decay_between(G[t], G[s0 + e]) : 0.f;
             row = t;
             col = s0;
         } else {
-            const floatx4 d = dots<Cf, NPL - 1>(q, 16 * bt, k, 16 * bs, lane);
             const int s = 16 * bs + m, t0 = 16 * bt + 4 * g;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = s <= t0 + e ? scale * d[e] * decay_between(G[t0 + e], G[s]) : 0.f;

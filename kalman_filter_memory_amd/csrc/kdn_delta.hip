@@ -274,8 +274,8 @@ template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hi
 // The same recurrence with everything a chunk needs prepared further ahead, one barrier
 // per chunk and the rows copied straight into LDS.  While the recurrence is at chunk c,
 //   helper 3       copies chunk c + 4 (rows behind the sequence's last: that row again;
-//                  beta 0 keeps them out of the state)
-//   helper 2       sums the decays of chunk c + 3, and forms P of chunk c + 1
+//                  beta 0 keeps them out of the state), and sums the decays of chunk c + 3
+//   helper 2       forms P of chunk c + 1
 //   helpers 0, 1   form the triangular system of chunk c + 2, and invert that of c + 1,
 //                  taking turns (a chunk stays with one of them)
 template <int DK, int DV, bool KEEP> struct AheadLds {
@@ -340,35 +340,16 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             const bf16_t* q = static_cast<const bf16_t*>(a.q) + sq.rq * DK;
             const bf16_t* k = static_cast<const bf16_t*>(a.k) + sq.rq * DK;
             const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + col0;
-            constexpr int kCopies = C * DK / 512 * (KEEP ? 1 : 2) + C * COLS / 512;
             const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), lv = lds_address(L.v);
-            auto copy = [&](int c, int s) {
+            float g = 0.f, be = 0.f;
+            auto fetch = [&](int c, int s) {  // the gates and rows of chunk c
+                const int t = c * C + (lane & 31);
+                g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
+                be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
                 const int rows = sq.len - c * C;
                 copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
                 if constexpr (!KEEP) copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
                 copy_rows<COLS, true>(v + size_t(c) * (C * DV), DV, rows, lv + s * (C * COLS * 2), lane);
-            };
-            if (nc > 0) copy(0, 0);
-            if (nc > 1) copy(1, 1);
-            copies_done<0>();
-            sync_lds();
-            int s = 2;
-            for (int c = -2; c < nc; ++c) {
-                if (c + 4 < nc) {
-                    copy(c + 4, s);
-                    copies_done<kCopies>();
-                } else {
-                    copies_done<0>();
-                }
-                s = s == 4 ? 0 : s + 1;
-                sync_lds();
-            }
-        } else if (hw == 2) {
-            float g = 0.f, be = 0.f;
-            auto gates = [&](int c) {
-                const int t = c * C + (lane & 31);
-                g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
-                be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
             };
             auto sums = [&](int c) {
                 const int s = c & 3;
@@ -381,16 +362,25 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
                     L.beta[s][lane] = be;
                 }
             };
-            gates(0);
-            sums(0);
-            gates(1);
+            if (nc > 0) {
+                fetch(0, 0);
+                sums(0);
+            }
+            if (nc > 1) fetch(1, 1);
+            copies_done<0>();
+            sync_lds();
+            int s = 2;
+            for (int c = -2; c < nc; ++c) {
+                copies_done<0>();  // chunk c + 3's rows (they had an interval)
+                if (c + 3 < nc) sums(c + 3);
+                if (c + 4 < nc) fetch(c + 4, s);
+                s = s == 4 ? 0 : s + 1;
+                sync_lds();
+            }
+        } else if (hw == 2) {
             sync_lds();
             int s = 4;  // where chunk c + 1 is
             for (int c = -2; c < nc; ++c) {
-                if (c + 3 < nc) {
-                    sums(c + 3);
-                    gates(c + 4);
-                }
                 if constexpr (!KEEP)
                     if (c >= -1 && c + 1 < nc)
                         readout_of<Cf, false, 2>(L.q[s], L.k[s], L.G[(c + 1) & 3], a.scale, L.p[(c + 1) & 1], lane);
@@ -439,16 +429,16 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             for (int e = 0; e < 4; ++e) f[4 * x + e] = o[e];
         }
     };
-    Planes<1> kf[2][KS], qf[2][KS];
+    Planes<1> kf[2][KS];
     auto fetch = [&](int s) {
 #pragma unroll
         for (int j = 0; j < KS; ++j)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
-                if constexpr (!KEEP) qf[x][j] = row_frag<Cf>(L.q[s], x, j, lane);
-            }
+            for (int x = 0; x < 2; ++x) kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
     };
+    bf16x8 minus[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) minus[x] = minus_unit(lane, x);
     int s = 0;
     if (nc > 0) fetch(0);
     for (int c = 0; c < nc; ++c) {
@@ -458,42 +448,94 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
                 keep_state<bf16_t, KS>(
                     st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK, col, lane);
         }
-        floatx4 ks[2], qs[2];
+        floatx4 gam[2], be[2], rest[2];
+        short4x vw[2];
+        Planes<3> tf[2];
+        Planes<1> qf[2][KS], kt[KT];
+        Planes<2> sp[KS];
+        floatx4 ks[2], qs[2], r1[2 * KS];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < 2; ++x) {
+            const int t = 8 * g + 4 * x;
+            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
+            vw[x] = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
+            ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        }
+        const float last = L.gam[sg][C - 1];
+        if constexpr (!KEEP)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) qf[x][j] = row_frag<Cf>(L.q[s], x, j, lane);
+        // planes of S (what a plane leaves: a product with minus the unit matrix), K S, and S
+        // scaled for its update
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-            const Planes<3> sp = state_planes<KT>(st, j);
+            sp[j].p[0] = pack8(st[2 * j], st[2 * j + 1]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) ks[x] = product<2>(kf[x][j], sp, ks[x]);
-            if constexpr (!KEEP)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) qs[x] = product<1>(qf[x][j], sp, qs[x]);
+            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j].p[0], st[2 * j + x]);
         }
-        if (c > 0) {  // the chunk before (a whole one)
+        if (c > 0) {  // results of the chunk before (a whole one)
             float f[8];
             results(f);
             bf16_t* p = out + size_t(c - 1) * (C * DV);
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e * DV] = f2bf(f[e]);
         }
-        floatx4 gam[2], be[2], rest[2];
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            sp[j].p[1] = pack8(r1[2 * j], r1[2 * j + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j].p[0], ks[x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j].p[1], r1[2 * j + x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[2 * j + x][e] *= last;
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            const bf16x8 p2 = pack8(r1[2 * j], r1[2 * j + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j].p[1], ks[x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], p2, ks[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tf[x] = square_frag<3>(L.t[c & 1], x, lane);
+        // R = V - gamma K S, beside Q S
+        if constexpr (!KEEP)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) qs[x] = Mma<bf16_t>::mma(qf[x][j].p[0], sp[j].p[0], qs[x]);
         float f[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * x + e] = bf2f(static_cast<bf16_t>(vw[x][e])) - gam[x][e] * ks[x][e];
+        const Planes<3> rp = split8<3>(f);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) kt[i] = col_frag<Cf>(L.k[s], i / 2, i % 2, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
-            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
             be[x] = *reinterpret_cast<const floatx4*>(&L.beta[sg][t]);
             rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[sg][t]);
-            const short4x w = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * x + e] = bf2f(static_cast<bf16_t>(w[e])) - gam[x][e] * ks[x][e];
         }
-        const Planes<3> rp = split8<3>(f);
+        // E = T R, beside the rest of Q S
         floatx4 ee[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-            ee[x] = product<2>(square_frag<3>(L.t[c & 1], x, lane), rp, floatx4{0.f, 0.f, 0.f, 0.f});
+        for (int x = 0; x < 2; ++x) ee[x] = product<2>(tf[x], rp, floatx4{0.f, 0.f, 0.f, 0.f});
+        if constexpr (!KEEP) {
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) qs[x] = Mma<bf16_t>::mma(qf[x][j].p[0], sp[j].p[1], qs[x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) lp[x] = square_frag<2>(L.p[c & 1], x, lane);
+        }
         float u[8], ub[8];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -501,20 +543,18 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             for (int e = 0; e < 4; ++e) {
                 u[4 * x + e] = be[x][e] * ee[x][e];
                 ub[4 * x + e] = rest[x][e] * u[4 * x + e];
-                left[x][e] = KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
             }
-        if constexpr (!KEEP) {
-            lu = split8<2>(u);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) lp[x] = square_frag<2>(L.p[c & 1], x, lane);
-        }
         const Planes<3> up = split8<3>(ub);
-        const float last = L.gam[sg][C - 1];
+        // S <- gamma_C S + K^T (rest U)
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            const floatx4 w = {last * st[i][0], last * st[i][1], last * st[i][2], last * st[i][3]};
-            st[i] = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), up, w);
-        }
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+            for (int i = 0; i < KT; ++i) st[i] = Mma<bf16_t>::mma(kt[i].p[0], up.p[n], st[i]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) left[x][e] = KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
+        if constexpr (!KEEP) lu = split8<2>(u);
         s = s == 4 ? 0 : s + 1;
         if (c + 1 < nc) fetch(s);
         sync_lds();
