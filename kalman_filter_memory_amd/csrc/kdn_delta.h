@@ -115,17 +115,33 @@ __device__ __forceinline__ bf16x8 pack8(floatx4 a, floatx4 b) {
     return __builtin_bit_cast(bf16x8, u32x4{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])});
 }
 
-// Minus the unit matrix for result tile h of a pair: minus_unit . pack8(a, b) + (a or b) is
-// what the rounding left, exactly, on the matrix unit instead of 8 vector instructions.
-__device__ __forceinline__ bf16x8 minus_unit(int lane, int h) {
+// The unit matrix, or minus it, that selects result tile h of a pair from the operand the
+// pair makes.  minus_unit . pack8(a, b) + (a or b) is what the rounding left, exactly, on
+// the matrix unit instead of 8 vector instructions.
+__device__ __forceinline__ bf16x8 unit(int lane, int h, uint32_t one = 0x3f80u) {
     u32x4 w = {0, 0, 0, 0};
     const int m = lane & 15, i = (m & 3) + 4 * h;
     if (m >> 2 == lane >> 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = i >> 1 == e ? ((i & 1) ? 0xbf800000u : 0x0000bf80u) : 0u;
+        for (int e = 0; e < 4; ++e) w[e] = i >> 1 == e ? ((i & 1) ? one << 16 : one) : 0u;
     }
     return __builtin_bit_cast(bf16x8, w);
 }
+__device__ __forceinline__ bf16x8 minus_unit(int lane, int h) { return unit(lane, h, 0xbf80u); }
+
+// Tile h of a pair of result tiles given as planes (tokens or key dimensions down, this
+// lane's column of d_v), turned over: lane l gets row paired_row(l, h) of the pair, the
+// columns 4 (l / 16) + 0..3.  Exact, as every plane is.
+template <int N> __device__ __forceinline__ floatx4 turned(const Planes<N>& x, bf16x8 u) {
+    floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n) c = Mma<bf16_t>::mma(x.p[n], u, c);
+    return c;
+}
+__device__ __forceinline__ void put4(bf16_t* p, floatx4 x) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+}
+__device__ __forceinline__ void put4(float* p, floatx4 x) { *reinterpret_cast<floatx4*>(p) = x; }
 
 // ------------------------------------------------------------------ token rows in LDS
 // Rows of D elements (a plane), the 16-byte pieces of row t stored at piece ^ f(t): both
@@ -331,6 +347,26 @@ template <typename E, int DK_, int W_> struct Cfg {
     using Tile = Rows<DK>;
 };
 
+// 16-byte pieces of a row of v's columns, swapped in every second pair of rows, so that
+// the four rows of a transposing read meet every bank once
+template <int COLS> __device__ __forceinline__ int value_at(int row, int piece) {
+    return row * COLS + ((piece ^ (((row >> 1) & 1) << 1)) << 3);
+}
+
+// Copies a chunk's 32 rows of D columns (in the order of Rows<D>, or of value_at) with one
+// wave: rows are `stride` elements apart, the last of `rows` stands in for those behind it.
+template <int D, bool VALUES>
+__device__ __forceinline__ void copy_rows(const bf16_t* x, unsigned stride, int rows, uint32_t lds, int lane) {
+    constexpr int kPer = D / 8, kRows = 64 / kPer;  // pieces of a row, rows of a copy
+#pragma unroll
+    for (int i = 0; i < C / kRows; ++i) {
+        const int row = kRows * i + lane / kPer, at = lane % kPer;
+        // the piece that belongs at place `at` (both orders are their own inverses)
+        const int piece = ((VALUES ? value_at<D>(row, at) : Rows<D>::at(row, at)) - row * D) >> 3;
+        copy_to_lds(x, unsigned(min(row, rows - 1)) * stride * 2u + unsigned(piece) * 16u, lds + 1024u * i);
+    }
+}
+
 // eight elements of a row, or zeros, raw
 template <typename E> struct Raw8 {
     static constexpr int N = sizeof(E) / 2;
@@ -432,10 +468,11 @@ __device__ __forceinline__ void system_of(const bf16_t* k, const LogSum* G, cons
 }
 
 // P_ts = scale Gamma_ts q_t.k_s (s <= t) in NPL planes of 32 x 32, or transposed.  The
-// block above the diagonal (below, transposed) must hold zeros already.
+// block above the diagonal (below, transposed) must hold zeros already.  Transposed, the
+// tokens from `rows` on get 0.
 template <typename Cf, bool TRANSPOSED, int NPL>
-__device__ __forceinline__ void readout_of(const bf16_t* q, const bf16_t* k, const LogSum* G, float scale, bf16_t* out,
-                                           int lane) {
+__device__ __forceinline__ void readout_of(const bf16_t* q, const bf16_t* k, const LogSum* G, float scale, int rows,
+                                           bf16_t* out, int lane) {
     const int m = lane & 15, g = lane >> 4;
     floatx4 all[3];
     if constexpr (TRANSPOSED) dots<Cf, NPL - 1, false>(q, k, all, lane);
@@ -455,7 +492,7 @@ __device__ __forceinline__ void readout_of(const bf16_t* q, const bf16_t* k, con
         } else {
             const int s = 16 * bs + m, t0 = 16 * bt + 4 * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = s <= t0 + e ? scale * d[e] * decay_between(G[t0 + e], G[s]) : 0.f;
+            for (int e = 0; e < 4; ++e) v[e] = s <= t0 + e && t0 + e < rows ? scale * d[e] * decay_between(G[t0 + e], G[s]) : 0.f;
             row = s;
             col = t0;
         }
@@ -525,12 +562,17 @@ template <int KS> __device__ __forceinline__ void store_state(const floatx4* st,
 // contraction runs over d_v; key dimensions in the order of paired_row): element (n, d)
 // with d = 32 j + 8 a + 4 h + b at
 //   ((n / 32) (DK / 16) + 2 j + h) 512 + (16 ((n % 32) / 8) + 4 a + b) 8 + n % 8
-template <typename E, int KS> __device__ __forceinline__ void keep_state(const floatx4* st, E* out, int n, int lane) {
-    E* p = out + (n >> 5) * (KS * 1024) + (16 * ((n & 31) >> 3) + 4 * (lane >> 4)) * 8 + (n & 7);
+template <typename E, int KS> __device__ __forceinline__ void keep_state(const floatx4 (&st)[2 * KS], E* out, int col0, int lane) {
+    const int n = col0 + 4 * (lane >> 4);  // this lane's columns of a turned tile
+    E* p = out + (n >> 5) * (KS * 1024) + (16 * ((n & 31) >> 3) + (lane & 15)) * 8 + (n & 7);
 #pragma unroll
-    for (int i = 0; i < 2 * KS; ++i)
+    for (int j = 0; j < KS; ++j) {
+        Planes<sizeof(E) == 2 ? 1 : 3> x;
+        if constexpr (sizeof(E) == 2) x.p[0] = pack8(st[2 * j], st[2 * j + 1]);
+        else x = state_planes<2 * KS>(st, j);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[i * 512 + e * 8] = from_f<E>(st[i][e]);
+        for (int h = 0; h < 2; ++h) put4(p + (2 * j + h) * 512, turned(x, unit(lane, h)));
+    }
 }
 
 // where the states at group gr of a sequence are kept (see group_count); `per` tokens a

@@ -117,7 +117,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
                 }
                 if constexpr (!KEEP) {
                     wave_lds_fence();
-                    readout_of<Cf, false, PP>(L.q[s], L.k[s], L.G[1], a.scale, L.p[s], lane);
+                    readout_of<Cf, false, PP>(L.q[s], L.k[s], L.G[1], a.scale, C, L.p[s], lane);
                 }
             }
         };
@@ -163,8 +163,8 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
         const int s = c & 1;
         if constexpr (KEEP) {
             if (c % a.group == 0)
-                keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col,
-                                  lane);
+                keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK,
+                                  col0 + 16 * wave, lane);
         }
         // K S (and Q S)
         floatx4 ks[2], qs[2];
@@ -291,26 +291,6 @@ template <int DK, int DV, bool KEEP> struct AheadLds {
     LogSum G[4][C];
 };
 
-// 16-byte pieces of a row of v's columns, swapped in every second pair of rows, so that
-// the four rows of a transposing read meet every bank once
-template <int COLS> __device__ __forceinline__ int value_at(int row, int piece) {
-    return row * COLS + ((piece ^ (((row >> 1) & 1) << 1)) << 3);
-}
-
-// Copies a chunk's 32 rows of D columns (in the order of Rows<D>, or of value_at) with one
-// wave: rows are `stride` elements apart, the last of `rows` stands in for those behind it.
-template <int D, bool VALUES>
-__device__ __forceinline__ void copy_rows(const bf16_t* x, unsigned stride, int rows, uint32_t lds, int lane) {
-    constexpr int kPer = D / 8, kRows = 64 / kPer;  // pieces of a row, rows of a copy
-#pragma unroll
-    for (int i = 0; i < C / kRows; ++i) {
-        const int row = kRows * i + lane / kPer, at = lane % kPer;
-        // the piece that belongs at place `at` (both orders are their own inverses)
-        const int piece = ((VALUES ? value_at<D>(row, at) : Rows<D>::at(row, at)) - row * D) >> 3;
-        copy_to_lds(x, unsigned(min(row, rows - 1)) * stride * 2u + unsigned(piece) * 16u, lds + 1024u * i);
-    }
-}
-
 template <int DK, int DV, bool KEEP>
 __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
     using Lds = AheadLds<DK, DV, KEEP>;
@@ -383,7 +363,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             for (int c = -2; c < nc; ++c) {
                 if constexpr (!KEEP)
                     if (c >= -1 && c + 1 < nc)
-                        readout_of<Cf, false, 2>(L.q[s], L.k[s], L.G[(c + 1) & 3], a.scale, L.p[(c + 1) & 1], lane);
+                        readout_of<Cf, false, 2>(L.q[s], L.k[s], L.G[(c + 1) & 3], a.scale, C, L.p[(c + 1) & 1], lane);
                 s = s == 4 ? 0 : s + 1;
                 sync_lds();
             }
@@ -413,21 +393,29 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
         for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
     const size_t groups = KEEP ? group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) : 0;
-    // this lane's outputs of a chunk: rows 8 g + 0..7 of its column
-    bf16_t* out = static_cast<bf16_t*>(KEEP ? a.keep_E : a.o) + (sq.rv + 8 * g) * DV + col;
+    bf16_t* out = static_cast<bf16_t*>(KEEP ? a.keep_E : a.o) + sq.rv * DV + col0 + 16 * wave + 4 * g;
     sync_lds();
     sync_lds();
     sync_lds();
     // What is left of a chunk when the state has gone on: o = scale gamma Q S + P U (or E)
     floatx4 left[2];
     Planes<2> lu, lp[2];
-    auto results = [&](float (&f)[8]) {
+    bf16x8 plus[2], minus[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const floatx4 o = KEEP ? left[x] : product<1>(lp[x], lu, left[x]);
+    for (int x = 0; x < 2; ++x) {
+        plus[x] = unit(lane, x);
+        minus[x] = minus_unit(lane, x);
+    }
+    // to the rows of chunk c, four columns of two rows from each lane
+    auto results = [&](int c, int rows) {
+        floatx4 o[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * x + e] = o[e];
-        }
+        for (int x = 0; x < 2; ++x) o[x] = KEEP ? left[x] : product<1>(lp[x], lu, left[x]);
+        const Planes<1> r = {{pack8(o[0], o[1])}};
+        bf16_t* p = out + size_t(c) * (C * DV);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (rows >= C || paired_row(lane, x) < rows) put4(p + paired_row(lane, x) * DV, turned(r, plus[x]));
     };
     Planes<1> kf[2][KS];
     auto fetch = [&](int s) {
@@ -436,9 +424,6 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
             for (int x = 0; x < 2; ++x) kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
     };
-    bf16x8 minus[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) minus[x] = minus_unit(lane, x);
     int s = 0;
     if (nc > 0) fetch(0);
     for (int c = 0; c < nc; ++c) {
@@ -446,7 +431,8 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
         if constexpr (KEEP) {
             if (c % a.group == 0)
                 keep_state<bf16_t, KS>(
-                    st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK, col, lane);
+                    st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK,
+                    col0 + 16 * wave, lane);
         }
         floatx4 gam[2], be[2], rest[2];
         short4x vw[2];
@@ -475,13 +461,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
             for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j].p[0], st[2 * j + x]);
         }
-        if (c > 0) {  // results of the chunk before (a whole one)
-            float f[8];
-            results(f);
-            bf16_t* p = out + size_t(c - 1) * (C * DV);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[e * DV] = f2bf(f[e]);
-        }
+        if (c > 0) results(c - 1, C);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
             sp[j].p[1] = pack8(r1[2 * j], r1[2 * j + 1]);
@@ -559,15 +539,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
         if (c + 1 < nc) fetch(s);
         sync_lds();
     }
-    if (nc > 0) {
-        float f[8];
-        results(f);
-        bf16_t* p = out + size_t(nc - 1) * (C * DV);
-        const int rows = sq.len - (nc - 1) * C - 8 * g;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < rows) p[e * DV] = f2bf(f[e]);
-    }
+    if (nc > 0) results(nc - 1, sq.len - (nc - 1) * C);
     if (a.S_T != nullptr) store_state<KS>(st, a.S_T + state, col, lane);
 }
 

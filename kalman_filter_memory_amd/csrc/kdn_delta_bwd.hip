@@ -131,7 +131,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
                     L.beta[s][lane] = be;
                 }
                 wave_lds_fence();
-                readout_of<Cf, true, 3>(L.q[s], L.k[s], L.G[1], a.scale, L.p[s], lane);
+                readout_of<Cf, true, 3>(L.q[s], L.k[s], L.G[1], a.scale, C, L.p[s], lane);
             }
         };
         int c = nc - 1;
@@ -179,7 +179,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
         const int s = c & 1, rows = sq.len - c * C;
         const size_t row0 = size_t(c) * C + 8 * g;
         if (c == nc - 1 || (c + 1) % a.group == 0)
-            keep_state<E, KS>(st, static_cast<E*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col, lane);
+            keep_state<E, KS>(st, static_cast<E*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col0 + 16 * wave, lane);
         float ev[8];  // E of this lane's tokens, 8 g + 0..7
 #pragma unroll
         for (int e = 0; e < 8; ++e) ev[e] = 8 * g + e < rows ? to_f<E>(Ep[(row0 + e) * a.dv]) : 0.f;
@@ -249,6 +249,282 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
         sync_lds();
         sync_lds();
     }
+    if (a.dS0 != nullptr) store_state<KS>(st, a.dS0 + state, col, lane);
+}
+
+// ---------------------------------------------------------------------- bfloat16 inputs
+// The backward recurrence with the chunks prepared ahead, as the forward one has them
+// (kdn_delta.hip).  Interval i is at chunk nc - 1 - i; helper 3 copies the rows of interval
+// i + 3 and sums the decays of i + 3, helper 2 forms P of i + 1, helpers 0 and 1 form the
+// system of i + 2 and invert that of i + 1.
+template <int DK, int DV> struct ReverseAheadLds {
+    static constexpr int W = DV == 32 ? 2 : 4, COLS = 16 * W;
+    bf16_t k[4][C * DK], q[4][C * DK];
+    bf16_t d[4][C * COLS], e[4][C * COLS];  // dO, E
+    bf16_t t[2][3 * C * C], p[2][3 * C * C];
+    float a[2][C * kLdA];
+    float tmp[2][32 * kLdT];
+    // gam[.][31] is the whole chunk's decay; zg = scale gam, 0 behind the last token
+    float gam[4][C], rest[4][C], beta[4][C], zg[4][C];
+    LogSum G[4][C];
+};
+
+template <int DK, int DV>
+__global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_reverse_ahead_kernel(BackwardArgs a) {
+    using Lds = ReverseAheadLds<DK, DV>;
+    constexpr int W = Lds::W, COLS = Lds::COLS;
+    using Cf = Cfg<bf16_t, DK, W>;
+    constexpr int KT = Cf::KT, KS = Cf::KS;
+    __shared__ __align__(16) Lds L;
+
+    constexpr unsigned slices = DV / COLS;
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
+    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int nc = (sq.len + C - 1) / C;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int col0 = slice * COLS;
+    const size_t state = (size_t(b) * a.H + h) * size_t(DV) * DK;
+
+    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += 64 * (W + 4))
+        reinterpret_cast<u32x4*>(L.t)[i] = reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
+
+    if (wave >= W) {
+        const int hw = wave - W;
+        if (hw == 3) {
+            const bf16_t* q = static_cast<const bf16_t*>(a.q) + sq.rq * DK;
+            const bf16_t* k = static_cast<const bf16_t*>(a.k) + sq.rq * DK;
+            const bf16_t* d = static_cast<const bf16_t*>(a.dO) + sq.rv * DV + col0;
+            const bf16_t* e = static_cast<const bf16_t*>(a.E) + sq.rv * DV + col0;
+            const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), ld = lds_address(L.d), le = lds_address(L.e);
+            float g = 0.f, be = 0.f;
+            auto gates = [&](int i) {
+                const int t = (nc - 1 - i) * C + (lane & 31);
+                g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
+                be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
+            };
+            auto copy = [&](int i) {
+                const int c = nc - 1 - i, s = i & 3, rows = sq.len - c * C;
+                copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
+                copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
+                copy_rows<COLS, true>(d + size_t(c) * (C * DV), DV, rows, ld + s * (C * COLS * 2), lane);
+                copy_rows<COLS, true>(e + size_t(c) * (C * DV), DV, rows, le + s * (C * COLS * 2), lane);
+            };
+            auto sums = [&](int i) {
+                const int s = i & 3;
+                const LogSum G = log_sums<C>(g, lane);
+                const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
+                if (lane < C) {
+                    const float gm = decay_of(G);
+                    L.G[s][lane] = G;
+                    L.gam[s][lane] = gm;
+                    L.rest[s][lane] = decay_between(last, G);
+                    L.beta[s][lane] = be;
+                    L.zg[s][lane] = (nc - 1 - i) * C + lane < sq.len ? a.scale * gm : 0.f;
+                }
+            };
+            if (nc > 0) {
+                gates(0);
+                copy(0);
+                sums(0);
+                gates(1 < nc ? 1 : 0);
+            }
+            copies_done<0>();
+            sync_lds();
+            for (int i = -2; i < nc; ++i) {
+                if (i + 3 < nc) {
+                    sums(i + 3);
+                    if (i + 4 < nc) gates(i + 4);
+                    copy(i + 3);
+                }
+                copies_done<0>();
+                sync_lds();
+            }
+        } else if (hw == 2) {
+            sync_lds();
+            for (int i = -2; i < nc; ++i) {
+                const int n = i + 1;
+                if (i >= -1 && n < nc)
+                    readout_of<Cf, true, 3>(L.q[n & 3], L.k[n & 3], L.G[n & 3], a.scale, sq.len - (nc - 1 - n) * C,
+                                            L.p[n & 1], lane);
+                sync_lds();
+            }
+        } else {
+            sync_lds();
+            for (int i = -2; i < nc; ++i) {
+                const int n = i + 2;
+                if ((i & 1) == hw) {
+                    if (n < nc) system_of<Cf, true>(L.k[n & 3], L.G[n & 3], L.beta[n & 3], L.a[hw], lane);
+                } else if (i >= -1 && i + 1 < nc) {
+                    invert<true>(L.a[hw], L.tmp[hw], L.t[(i + 1) & 1], lane);
+                }
+                sync_lds();
+            }
+        }
+        return;
+    }
+
+    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
+    floatx4 st[KT];
+    if (a.dS_T != nullptr) {
+        load_state<KS>(st, a.dS_T + state, col, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    const size_t groups = group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C));
+    bf16_t* dV = static_cast<bf16_t*>(a.dv_out) + sq.rv * DV + col0 + 16 * wave + 4 * g;
+    float* part = a.part + size_t(col0 / 16 + wave) * a.rows + sq.rv;
+    bf16x8 plus[2], minus[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        plus[x] = unit(lane, x);
+        minus[x] = minus_unit(lane, x);
+    }
+    // what is left of a chunk when the state has gone on: rows of dV, and dbeta's part
+    Planes<1> dv_left;
+    float db[8];
+    auto results = [&](int c, int rows) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (rows >= C || paired_row(lane, x) < rows)
+                put4(dV + (size_t(c) * C + paired_row(lane, x)) * DV, turned(dv_left, plus[x]));
+        // sums over the 16 columns; lane m < 8 of a group takes token 8 g + m
+#pragma unroll
+        for (int i = 0; i < 8; ++i) db[i] = group_sum<16>(db[i]);
+        float v = (m & 1) ? db[1] : db[0];
+        v = (m & 6) == 2 ? ((m & 1) ? db[3] : db[2]) : v;
+        v = (m & 6) == 4 ? ((m & 1) ? db[5] : db[4]) : v;
+        v = (m & 6) == 6 ? ((m & 1) ? db[7] : db[6]) : v;
+        if (m < 8 && 8 * g + m < rows) part[size_t(c) * C + 8 * g + m] = v;
+    };
+    sync_lds();
+    sync_lds();
+    sync_lds();
+    Planes<1> kf[2][KS];
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
+    };
+    if (nc > 0) fetch(0);
+    for (int i = 0; i < nc; ++i) {
+        const int c = nc - 1 - i, s = i & 3;
+        if (i == 0 || (c + 1) % a.group == 0)
+            keep_state<bf16_t, KS>(st, static_cast<bf16_t*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK,
+                                   col0 + 16 * wave, lane);
+        const float last = L.gam[s][C - 1];
+        Planes<1> dp;  // dO, tokens along the contraction
+        {
+            short4x w[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                w[x] = read_tr16(L.d[s] + value_at<COLS>(8 * g + 4 * x + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
+            const short8x v = {w[0][0], w[0][1], w[0][2], w[0][3], w[1][0], w[1][1], w[1][2], w[1][3]};
+            dp.p[0] = __builtin_bit_cast(bf16x8, v);
+        }
+        Planes<3> pf[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) pf[x] = square_frag<3>(L.p[i & 1], x, lane);
+        float z[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const floatx4 w = *reinterpret_cast<const floatx4*>(&L.zg[s][8 * g + 4 * x]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[4 * x + e] = w[e];
+        }
+        // planes of D, K D, P^T dO
+        floatx4 kd[2], pd[2], r1[KT];
+        bf16x8 sp[KS];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) kd[x] = pd[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            sp[j] = pack8(st[2 * j], st[2 * j + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j], st[2 * j + x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) kd[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j], kd[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) pd[x] = product<2>(pf[x], dp, pd[x]);
+        if (i > 0) results(c + 1, i == 1 ? sq.len - (nc - 1) * C : C);
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            sp[j] = pack8(r1[2 * j], r1[2 * j + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j], r1[2 * j + x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) kd[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j], kd[x]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[2 * j + x][e] *= last;
+        }
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            const bf16x8 p2 = pack8(r1[2 * j], r1[2 * j + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) kd[x] = Mma<bf16_t>::mma(kf[x][j].p[0], p2, kd[x]);
+        }
+        // D <- gamma_C D + Q^T (scale gamma dO), beside the way to X
+        {
+            float f[8];
+            join8<1>(dp, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] *= f[e];
+        }
+        const Planes<3> zp = split8<3>(z);
+        Planes<3> tf[2];
+        float rest[8], be[8], gam[8], ev[8], f[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int t = 8 * g + 4 * x;
+            tf[x] = square_frag<3>(L.t[i & 1], x, lane);
+            const floatx4 rs = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
+            const floatx4 bt = *reinterpret_cast<const floatx4*>(&L.beta[s][t]);
+            const floatx4 gm = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
+            const short4x w = read_tr16(L.e[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                rest[4 * x + e] = rs[e];
+                be[4 * x + e] = bt[e];
+                gam[4 * x + e] = gm[e];
+                ev[4 * x + e] = bf2f(static_cast<bf16_t>(w[e]));
+                f[4 * x + e] = fmaf(rest[4 * x + e], kd[x][e], pd[x][e]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KT; ++j) st[j] = product<2>(col_frag<Cf>(L.q[s], j / 2, j % 2, lane), zp, st[j]);
+        // X = T^T dU
+        const Planes<3> up = split8<3>(f);
+        floatx4 xx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) xx[x] = product<2>(tf[x], up, floatx4{0.f, 0.f, 0.f, 0.f});
+        // D <- D - K^T (gamma dV)
+        floatx4 w[2];
+        float y[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = 4 * x + e;
+                w[x][e] = be[n] * xx[x][e];
+                y[n] = -gam[n] * w[x][e];
+                db[n] = xx[x][e] * ev[n];
+            }
+        dv_left.p[0] = pack8(w[0], w[1]);
+        const Planes<3> yp = split8<3>(y);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+                st[j] = Mma<bf16_t>::mma(col_frag<Cf>(L.k[s], j / 2, j % 2, lane).p[0], yp.p[n], st[j]);
+        if (i + 1 < nc) fetch((i + 1) & 3);
+        sync_lds();
+    }
+    if (nc > 0) results(0, nc == 1 ? sq.len : C);
     if (a.dS0 != nullptr) store_state<KS>(st, a.dS0 + state, col, lane);
 }
 
@@ -541,7 +817,8 @@ __global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads)) void delta_grad_ker
 template <typename E, int DK, int DV> void backward_d(const BackwardArgs& a, size_t slots, hipStream_t st) {
     constexpr int W = DV == 32 ? 2 : 4;
     const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
-    delta_reverse_kernel<E, DK, W><<<n, Cfg<E, DK, W>::kThreads, 0, st>>>(a);
+    if constexpr (sizeof(E) == 2) delta_reverse_ahead_kernel<DK, DV><<<n, 64 * (W + 4), 0, st>>>(a);
+    else delta_reverse_kernel<E, DK, W><<<n, Cfg<E, DK, W>::kThreads, 0, st>>>(a);
     delta_grad_kernel<E, DK, DV><<<unsigned(slots * a.Hk), GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
 }
 template <typename E, int DK> void backward_k(const BackwardArgs& a, size_t slots, hipStream_t st) {
