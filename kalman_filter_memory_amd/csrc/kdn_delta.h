@@ -145,13 +145,14 @@ __device__ __forceinline__ void put4(float* p, floatx4 x) { *reinterpret_cast<fl
 
 // ------------------------------------------------------------------ token rows in LDS
 // Rows of D elements (a plane), the 16-byte pieces of row t stored at piece ^ f(t): both
-// the row-wise fragments (pieces of 16 rows) and the transposing reads (4 pieces of 4
-// rows) then meet every bank once at D = 128.
+// the row-wise fragments (a piece of rows 8 a + 0..3, or of 8 neighbours) and the
+// transposing reads (4 pieces of 4 rows) then meet every bank once.
 template <int D> struct Rows {
     static constexpr int kPieces = D / 8;
     static __device__ __forceinline__ int at(int row, int piece) {
-        const int f = ((row & 3) << 2) | (((row >> 2) ^ (row >> 3)) & 3);
-        return row * D + ((piece ^ (f & (kPieces - 1))) << 3);
+        const int x = ((row >> 2) ^ (row >> 3)) & 3;
+        const int f = kPieces == 16 ? (((row & 3) << 2) | x) : kPieces == 8 ? (((row & 2) << 1) | x) : x;
+        return row * D + ((piece ^ f) << 3);
     }
     // operand rows of this lane: the row's 8 elements of `piece`
     static __device__ __forceinline__ bf16x8 row(const bf16_t* x, int row, int piece) {
@@ -389,10 +390,10 @@ template <typename E> __device__ __forceinline__ Planes<sizeof(E) == 2 ? 1 : 3> 
     }
 }
 
-// Token rows x[row0 + 0..31][0..D) on their way to LDS through the helper waves'
+// Token rows x[row0 + 0 .. ROWS - 1][0..D) on their way to LDS through the helper waves'
 // registers: thread `h` of 64 NH holds N pieces.
-template <typename E, int D, int THREADS> struct Stage {
-    static constexpr int kPer = D / 8, kAll = C * kPer, N = (kAll + THREADS - 1) / THREADS;
+template <typename E, int D, int THREADS, int ROWS = C> struct Stage {
+    static constexpr int kPer = D / 8, kAll = ROWS * kPer, N = (kAll + THREADS - 1) / THREADS;
     Raw8<E> r[N];
     __device__ __forceinline__ void load(const E* x, size_t stride, int rows, int h) {
 #pragma unroll

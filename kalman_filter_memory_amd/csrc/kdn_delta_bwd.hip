@@ -530,49 +530,91 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
 
 // -------------------------------------------------------------------------- gradients
 // A workgroup takes one group of tokens of one head of queries and keys, and the heads of
-// values that share it one after the other.  A wave holds 16 key dimensions of dQ and dK
-// (in the order of paired_row) for all tokens of the group.
+// values that share it one after the other.  A wave holds TD x 16 key dimensions of dQ and
+// dK for all tokens of the group, key dimensions down and tokens across (in the order of
+// paired_row both), so that gates are one number per lane and rows leave in pieces of four
+// columns.  d_v is taken PASS columns at a time.
 template <typename E, int DK, int DV> struct GradCfg {
-    static constexpr int NP = sizeof(E) == 2 ? 1 : 3;
-    static constexpr int G = sizeof(E) == 2 ? 64 : 32;  // tokens of a group
-    static constexpr int NW = DK / 16, kThreads = 64 * NW;
-    static constexpr int NJ = G / 32, NN = DV / 32;  // steps over the tokens, over d_v
+    static constexpr bool kPlain = sizeof(E) == 2;
+    static constexpr int NP = kPlain ? 1 : 3;
+    static constexpr int G = kPlain ? 64 : 32;  // tokens of a group
+    static constexpr int TD = DK == 128 ? 2 : 1;
+    static constexpr int NW = DK / 16 / TD, kThreads = 64 * NW;
+    static constexpr int PASS = kPlain && DV > 32 ? 64 : 32, kPasses = DV / PASS, NS = PASS / 32;
+    static constexpr int NJ = G / 32, NX = 2 * NJ;           // pairs of token tiles, tiles
+    static constexpr int NB = G / 16, NBLK = NB * (NB + 1) / 2;  // blocks on and below the diagonal
+    static constexpr int NJOB = (2 * NBLK + NW - 1) / NW;    // of dP and M together, for a wave
     using KRow = Rows<DK>;
-    using VRow = Rows<DV>;
+    using VRow = Rows<PASS>;
     using MRow = Rows<G>;
 };
 template <typename E, int DK, int DV> struct GradLds {
     using Cf = GradCfg<E, DK, DV>;
+    static constexpr int kTile = Cf::NP * Cf::G * Cf::PASS, kSquare = Cf::NP * Cf::G * Cf::G;
     bf16_t q[Cf::NP * Cf::G * DK], k[Cf::NP * Cf::G * DK];
-    bf16_t o[Cf::NP * Cf::G * DV], u[Cf::NP * Cf::G * DV], v[Cf::NP * Cf::G * DV];  // dO, U, dV
-    bf16_t p[Cf::NP * Cf::G * Cf::G], m[Cf::NP * Cf::G * Cf::G];                    // dP and M, [s][t]
+    union {
+        bf16_t rows[3][kTile];   // dO, E, dV: a pass
+        bf16_t square[2][kSquare];  // then dP and M, [t][s]
+    };
     LogSum sum[Cf::G];
-    float gam[Cf::G], rest[Cf::G];
+    float gam[Cf::G], rest[Cf::G], beta[Cf::G];
     float red[Cf::NW][Cf::G], ds[Cf::NW];
-    float wr[Cf::G / 8][Cf::G], wc[Cf::G / 8][Cf::G];  // W's row and column sums by blocks, of dP's part and of M's
+    float wr[2 * Cf::NB][Cf::G], wc[2 * Cf::NB][Cf::G];  // row and column sums of W by blocks, of dP's part and of M's
 };
 
-template <typename Row, int NP, int G, int D>
+template <typename Row, int NP, int SIZE>
 __device__ __forceinline__ Planes<NP> rows_at(const bf16_t* x, int row, int piece) {
     Planes<NP> r;
 #pragma unroll
-    for (int n = 0; n < NP; ++n) r.p[n] = Row::row(x + n * G * D, row, piece);
+    for (int n = 0; n < NP; ++n) r.p[n] = Row::row(x + n * SIZE, row, piece);
     return r;
 }
-template <typename Row, int NP, int G, int D>
+template <typename Row, int NP, int SIZE>
 __device__ __forceinline__ Planes<NP> cols_at(const bf16_t* x, int t0, int j, int h, int lane) {
     Planes<NP> r;
 #pragma unroll
-    for (int n = 0; n < NP; ++n) r.p[n] = Row::col(x + n * G * D, t0, j, h, lane);
+    for (int n = 0; n < NP; ++n) r.p[n] = Row::col(x + n * SIZE, t0, j, h, lane);
     return r;
 }
 
-template <typename E, int DK, int DV>
-__global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads)) void delta_grad_kernel(BackwardArgs a) {
+// ROWS rows of D columns into LDS as planes, in the order of Rows<D>, by all waves: copied
+// where the type is bfloat16 (rows from `rows` on: the last one again), else through
+// registers (zeros behind the last).
+template <typename E, int D, int ROWS, int NW>
+__device__ __forceinline__ void rows_to_lds(const E* x, unsigned stride, int rows, bf16_t* out, int wave, int lane) {
+    if constexpr (sizeof(E) == 2) {
+        constexpr int kPer = D / 8, kRows = 64 / kPer, N = ROWS / kRows;
+        const uint32_t lds = lds_address(out);
+#pragma unroll
+        for (int i = 0; i < (N + NW - 1) / NW; ++i) {
+            const int c = wave + NW * i;
+            if (N % NW == 0 || c < N) {
+                const int row = kRows * c + lane / kPer, at = lane % kPer;
+                const int piece = (Rows<D>::at(row, at) - row * D) >> 3;
+                copy_to_lds(x, unsigned(min(row, rows - 1)) * stride * 2u + unsigned(piece) * 16u, lds + 1024u * unsigned(c));
+            }
+        }
+    } else {
+        Stage<E, D, 64 * NW, ROWS> st;
+        const int t = 64 * wave + lane;
+        st.load(x, stride, rows, t);
+        st.each(t, [&](const Raw8<E>& r, int row, int p) {
+            const auto y = planes_of<E>(r);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(out + n * ROWS * D + Rows<D>::at(row, p)) = y.p[n];
+        });
+    }
+}
+
+// SHARED: several heads of values share the head of keys.
+template <typename E, int DK, int DV, bool SHARED>
+__global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads), 2) void delta_grad_kernel(BackwardArgs a) {
     using Cf = GradCfg<E, DK, DV>;
-    constexpr int NP = Cf::NP, G = Cf::G, NW = Cf::NW, NJ = Cf::NJ, NN = Cf::NN, LIM = NP - 1;
-    __shared__ __align__(16) GradLds<E, DK, DV> L;
-    const int lane = threadIdx.x & 63, wave = wave_id(), tid = threadIdx.x;
+    using Lds = GradLds<E, DK, DV>;
+    constexpr int NP = Cf::NP, G = Cf::G, NW = Cf::NW, NJ = Cf::NJ, NX = Cf::NX, NS = Cf::NS, LIM = NP - 1, TD = Cf::TD;
+    constexpr int PASS = Cf::PASS, NB = Cf::NB, NBLK = Cf::NBLK, KSIZE = G * DK, VSIZE = G * PASS, MSIZE = G * G;
+    __shared__ __align__(16) Lds L;
+    const int lane = threadIdx.x & 63, wave = wave_id();
     const int g = lane >> 4, m = lane & 15;
     const int groups_T = (a.T + G - 1) / G;
     const unsigned id = xcd_order(blockIdx.x, gridDim.x);
@@ -599,178 +641,235 @@ __global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads)) void delta_grad_ker
     const size_t rq = s0.rq + t0;
     const size_t place = group_slot(a.cu, b, s0.start, G, groups_T) + gr;
 
-    // Q and K; zeros where dP and M are never written
-    const E* qp = static_cast<const E*>(a.q) + rq * DK;
-    const E* kp = static_cast<const E*>(a.k) + rq * DK;
-    for (int e = tid; e < G * DK / 8; e += Cf::kThreads) {
-        const int row = e / (DK / 8), p = e % (DK / 8);
-        const auto x = planes_of<E>(load_raw8<E>(qp + size_t(row) * DK + 8 * p, row < rows));
-        const auto y = planes_of<E>(load_raw8<E>(kp + size_t(row) * DK + 8 * p, row < rows));
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            *reinterpret_cast<bf16x8*>(L.q + n * G * DK + Cf::KRow::at(row, p)) = x.p[n];
-            *reinterpret_cast<bf16x8*>(L.k + n * G * DK + Cf::KRow::at(row, p)) = y.p[n];
-        }
-    }
-    for (int e = tid; e < NP * G * G / 8; e += Cf::kThreads)
-        reinterpret_cast<u32x4*>(L.p)[e] = reinterpret_cast<u32x4*>(L.m)[e] = u32x4{0, 0, 0, 0};
+    rows_to_lds<E, DK, G, NW>(static_cast<const E*>(a.q) + rq * DK, DK, rows, L.q, wave, lane);
+    rows_to_lds<E, DK, G, NW>(static_cast<const E*>(a.k) + rq * DK, DK, rows, L.k, wave, lane);
 
-    const int wj = wave >> 1, wh = wave & 1;  // this wave's key dimensions: 32 wj + paired_row(., wh)
-    floatx4 dq[2 * NJ], dk[2 * NJ];
+    floatx4 dq[SHARED ? TD : 1][SHARED ? NX : 1], dk[SHARED ? TD : 1][SHARED ? NX : 1];
+    if constexpr (SHARED)
 #pragma unroll
-    for (int x = 0; x < 2 * NJ; ++x) dq[x] = dk[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int d = 0; d < TD; ++d)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) dq[d][x] = dk[d][x] = floatx4{0.f, 0.f, 0.f, 0.f};
 
     for (int hv = 0; hv < r; ++hv) {
         const int h = hk * r + hv;
         const size_t rv = sequence(a.cu, b, h, a.H, a.Hk, a.T).rv + t0;
         const E* Sp = static_cast<const E*>(a.S) + (place * a.H + h) * size_t(DV) * DK;
         const E* Dp = static_cast<const E*>(a.D) + (place * a.H + h) * size_t(DV) * DK;
-        __syncthreads();  // the tiles of the head before are done with
-        if (wave == 0) {
-            const bool in = lane < rows && lane < G;
-            const LogSum x = log_sums<G>(in ? load_gate(a.g, rv + lane, a.gate_bf16) : 0.f, lane);
-            const LogSum last = {lane_value(x.hi, G - 1), lane_value(x.lo, G - 1)};
-            if (lane < G) {
-                L.sum[lane] = x;
-                L.gam[lane] = decay_of(x);
-                L.rest[lane] = decay_between(last, x);
-            }
-        }
-        constexpr int kPer = DV / 8;
-        for (int e = tid; e < G * kPer; e += Cf::kThreads) {
-            const int row = e / kPer, p = e % kPer;
-            const size_t at = (rv + row) * DV + 8 * p;
-            const bool ok = row < rows;
-            const auto xo = planes_of<E>(load_raw8<E>(static_cast<const E*>(a.dO) + at, ok));
-            const auto xv = planes_of<E>(load_raw8<E>(static_cast<const E*>(a.dv_out) + at, ok));
-            const auto ee = planes_of<E>(load_raw8<E>(static_cast<const E*>(a.E) + at, ok));
-            const float bt = ok ? load_gate(a.beta, rv + row, a.gate_bf16) : 0.f;
-            float f[8];
-            join8<NP>(ee, f);
+        if (SHARED && hv > 0) __syncthreads();  // the head before is done with its tiles and gates
+        floatx4 os[TD][NX], vs[TD][NX], ed[TD][NX], xt[Cf::NJOB];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] *= bt;
-            const Planes<NP> xu = split8<NP>(f);
+        for (int d = 0; d < TD; ++d)
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                const int at2 = n * G * DV + Cf::VRow::at(row, p);
-                *reinterpret_cast<bf16x8*>(L.o + at2) = xo.p[n];
-                *reinterpret_cast<bf16x8*>(L.v + at2) = xv.p[n];
-                *reinterpret_cast<bf16x8*>(L.u + at2) = xu.p[n];
-            }
-        }
-        __syncthreads();
-        // dP and M, blocks of 16 x 16 on and below the diagonal, dealt to the waves
-        constexpr int NB = G / 16, NBLK = NB * (NB + 1) / 2, KSTEPS = DK / 32;
-        for (int x = wave; x < 2 * NBLK; x += NW) {
-            const bool is_p = x < NBLK;
-            int y = is_p ? x : x - NBLK, bt = 0;
-            while (y > bt) y -= ++bt;
-            const int bs = y;
-            floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int x = 0; x < NX; ++x) os[d][x] = vs[d][x] = ed[d][x] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < NN; ++j)
-                acc = product<LIM>(rows_at<typename Cf::VRow, NP, G, DV>(is_p ? L.o : L.v, 16 * bt + m, 4 * j + g),
-                                   rows_at<typename Cf::VRow, NP, G, DV>(L.u, 16 * bs + m, 4 * j + g), acc);
-            floatx4 qk = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < KSTEPS; ++j)
-                qk = product<LIM>(rows_at<typename Cf::KRow, NP, G, DK>(is_p ? L.q : L.k, 16 * bt + m, 4 * j + g),
-                                  rows_at<typename Cf::KRow, NP, G, DK>(L.k, 16 * bs + m, 4 * j + g), qk);
-            const int s = 16 * bs + m, t = 16 * bt + 4 * g;  // (tokens behind the last have zeros in dO, dV and U)
-            float f[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool keep = is_p ? s <= t + e : s < t + e;
-                f[e] = keep ? (is_p ? a.scale : -1.f) * acc[e] * decay_between(L.sum[t + e], L.sum[s]) : 0.f;
-            }
-            float col = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float w = f[e] * qk[e];
-                col += w;
-                const float row = group_sum<16>(w);
-                if (m == e) L.wr[(is_p ? 0 : NB) + bs][t + e] = row;
-            }
-            col += __shfl_xor(col, 16, 64);
-            col += __shfl_xor(col, 32, 64);
-            if (g == 0) L.wc[(is_p ? 0 : NB) + bt][s] = col;
-            uint2 w[NP];
-            split4<NP>(f, w);
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-                *reinterpret_cast<uint2*>((is_p ? L.p : L.m) + n * G * G + Cf::MRow::at(s, t >> 3) + (t & 7)) = w[n];
-        }
-        // dO S, dV S and U D
-        floatx4 os[2 * NJ], vs[2 * NJ], ud[2 * NJ];
-#pragma unroll
-        for (int x = 0; x < 2 * NJ; ++x) os[x] = vs[x] = ud[x] = floatx4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < Cf::NJOB; ++i) xt[i] = floatx4{0.f, 0.f, 0.f, 0.f};
         float along = 0.f;  // <D, S>
+        float gate = 0.f, be = 0.f;
+        if (wave == 0 && lane < rows && lane < G) {
+            gate = load_gate(a.g, rv + lane, a.gate_bf16);
+            be = load_gate(a.beta, rv + lane, a.gate_bf16);
+        }
+#pragma unroll 1
+        for (int pass = 0; pass < Cf::kPasses; ++pass) {
+            if (pass > 0) __syncthreads();  // the pass before is done with the rows
+            const size_t at = rv * DV + pass * PASS;
+            rows_to_lds<E, PASS, G, NW>(static_cast<const E*>(a.dO) + at, DV, rows, L.rows[0], wave, lane);
+            rows_to_lds<E, PASS, G, NW>(static_cast<const E*>(a.E) + at, DV, rows, L.rows[1], wave, lane);
+            rows_to_lds<E, PASS, G, NW>(static_cast<const E*>(a.dv_out) + at, DV, rows, L.rows[2], wave, lane);
+            Raw8<E> sr[NS][TD], dr[NS][TD];
 #pragma unroll
-        for (int j = 0; j < NN; ++j) {
-            const size_t at = size_t(j * (DK / 16) + wave) * 512 + lane * 8;
-            const Planes<NP> sf = planes_of<E>(load_raw8<E>(Sp + at, true)), df = planes_of<E>(load_raw8<E>(Dp + at, true));
-            float x8[8], y8[8];
-            join8<NP>(sf, x8);
-            join8<NP>(df, y8);
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) along = fmaf(x8[i], y8[i], along);
+                for (int d = 0; d < TD; ++d) {
+                    const size_t f = size_t((pass * NS + j) * (DK / 16) + TD * wave + d) * 512 + lane * 8;
+                    sr[j][d] = load_raw8<E>(Sp + f, true);
+                    dr[j][d] = load_raw8<E>(Dp + f, true);
+                }
+            if (pass == 0 && wave == 0) {
+                const LogSum x = log_sums<G>(gate, lane);
+                const LogSum last = {lane_value(x.hi, G - 1), lane_value(x.lo, G - 1)};
+                if (lane < G) {
+                    // tokens behind the last: no decay, and no part in any product
+                    L.sum[lane] = x;
+                    L.gam[lane] = lane < rows ? decay_of(x) : 0.f;
+                    L.rest[lane] = lane < rows ? decay_between(last, x) : 0.f;
+                    L.beta[lane] = be;
+                }
+            }
+            copies_done<0>();
+            __syncthreads();
 #pragma unroll
-            for (int x = 0; x < 2 * NJ; ++x) {
-                const int row = 32 * (x >> 1) + paired_row(lane, x & 1), pc = 4 * j + g;
-                os[x] = product<LIM>(rows_at<typename Cf::VRow, NP, G, DV>(L.o, row, pc), sf, os[x]);
-                vs[x] = product<LIM>(rows_at<typename Cf::VRow, NP, G, DV>(L.v, row, pc), sf, vs[x]);
-                ud[x] = product<LIM>(rows_at<typename Cf::VRow, NP, G, DV>(L.u, row, pc), df, ud[x]);
+            for (int i = 0; i < Cf::NJOB; ++i) {
+                const int job = wave + NW * i;
+                if (2 * NBLK % NW == 0 || job < 2 * NBLK) {
+                    const bool is_p = job < NBLK;
+                    int y = is_p ? job : job - NBLK, bt = 0;
+                    while (y > bt) y -= ++bt;
+#pragma unroll
+                    for (int j = 0; j < NS; ++j)
+                        xt[i] = product<LIM>(rows_at<typename Cf::VRow, NP, VSIZE>(L.rows[1], 16 * y + m, 4 * j + g),
+                                             rows_at<typename Cf::VRow, NP, VSIZE>(L.rows[is_p ? 0 : 2], 16 * bt + m, 4 * j + g),
+                                             xt[i]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                Planes<NP> sf[TD], df[TD];
+#pragma unroll
+                for (int d = 0; d < TD; ++d) {
+                    sf[d] = planes_of<E>(sr[j][d]);
+                    df[d] = planes_of<E>(dr[j][d]);
+                    float x8[8], y8[8];
+                    join8<NP>(sf[d], x8);
+                    join8<NP>(df[d], y8);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) along = fmaf(x8[i], y8[i], along);
+                }
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int row = 32 * (x >> 1) + paired_row(lane, x & 1), pc = 4 * j + g;
+                    const Planes<NP> fo = rows_at<typename Cf::VRow, NP, VSIZE>(L.rows[0], row, pc);
+                    const Planes<NP> fe = rows_at<typename Cf::VRow, NP, VSIZE>(L.rows[1], row, pc);
+                    const Planes<NP> fv = rows_at<typename Cf::VRow, NP, VSIZE>(L.rows[2], row, pc);
+#pragma unroll
+                    for (int d = 0; d < TD; ++d) {
+                        os[d][x] = product<LIM>(sf[d], fo, os[d][x]);
+                        vs[d][x] = product<LIM>(sf[d], fv, vs[d][x]);
+                        ed[d][x] = product<LIM>(df[d], fe, ed[d][x]);
+                    }
+                }
             }
         }
-        along *= L.gam[G - 1];
-        __syncthreads();  // dP and M are there
-        float qsum[8 * NJ];
+        along *= L.gam[min(G, rows) - 1];
+        __syncthreads();  // the rows' place is for dP and M now
+        // zeros above the diagonal, where the products below read whole blocks of 32
+        for (int i = threadIdx.x; i < 2 * Lds::kSquare / 8; i += Cf::kThreads) {
+            const int e = i % (G * G / 8), row = e / (G / 8), p = (Cf::MRow::at(row, e % (G / 8)) - row * G) >> 3;
+            if (p >> 1 > row >> 4) reinterpret_cast<u32x4*>(L.square[0])[i] = u32x4{0, 0, 0, 0};
+        }
+        // dP = scale dO U^T Gamma, M = -dV U^T Gamma with U = beta E: this lane's column is t
 #pragma unroll
-        for (int jt = 0; jt < NJ; ++jt) {
-            float qv[8], kv[8];
-            join8<NP>(cols_at<typename Cf::KRow, NP, G, DK>(L.q, 32 * jt, wj, wh, lane), qv);
-            join8<NP>(cols_at<typename Cf::KRow, NP, G, DK>(L.k, 32 * jt, wj, wh, lane), kv);
+        for (int i = 0; i < Cf::NJOB; ++i) {
+            const int job = wave + NW * i;
+            if (2 * NBLK % NW == 0 || job < 2 * NBLK) {
+                const bool is_p = job < NBLK;
+                int y = is_p ? job : job - NBLK, bt = 0;
+                while (y > bt) y -= ++bt;
+                floatx4 qk = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int x = 2 * jt + hh;
-                floatx4 aq, ak = dk[x];
+                for (int j = 0; j < DK / 32; ++j)
+                    qk = product<LIM>(rows_at<typename Cf::KRow, NP, KSIZE>(L.k, 16 * y + m, 4 * j + g),
+                                      rows_at<typename Cf::KRow, NP, KSIZE>(is_p ? L.q : L.k, 16 * bt + m, 4 * j + g), qk);
+                const int t = 16 * bt + m, s = 16 * y + 4 * g;
+                float f[4], row = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = 32 * jt + 8 * g + 4 * hh + e;
-                    const float gm = L.gam[t], rs = L.rest[t];
-                    aq[e] = a.scale * gm * os[x][e];
-                    ak[e] += rs * ud[x][e] - gm * vs[x][e];
-                    const float into = kv[4 * hh + e] * rs * ud[x][e];
-                    along += into;
-                    qsum[8 * jt + 4 * hh + e] = gm * (a.scale * qv[4 * hh + e] * os[x][e] - kv[4 * hh + e] * vs[x][e]) - into;
+                    const bool keep = t < rows && (is_p ? s + e <= t : s + e < t);
+                    const float w = (is_p ? a.scale : -1.f) * L.beta[s + e] * decay_between(L.sum[t], L.sum[s + e]);
+                    f[e] = keep ? w * xt[i][e] : 0.f;
+                    const float wq = f[e] * qk[e];
+                    row += wq;
+                    const float col = group_sum<16>(wq);
+                    if (m == e) L.wc[(is_p ? 0 : NB) + bt][s + e] = col;
                 }
+                row += __shfl_xor(row, 16, 64);
+                row += __shfl_xor(row, 32, 64);
+                if (g == 0) L.wr[(is_p ? 0 : NB) + y][t] = row;
+                uint2 w[NP];
+                split4<NP>(f, w);
 #pragma unroll
-                for (int js = 0; js < NJ; ++js) {
-                    const Planes<NP> kf = cols_at<typename Cf::KRow, NP, G, DK>(L.k, 32 * js, wj, wh, lane);
-                    if (js <= jt) {  // rows t, contraction over s
-                        aq = product<LIM>(cols_at<typename Cf::MRow, NP, G, G>(L.p, 32 * js, jt, hh, lane), kf, aq);
-                        ak = product<LIM>(cols_at<typename Cf::MRow, NP, G, G>(L.m, 32 * js, jt, hh, lane), kf, ak);
-                    }
-                    if (js >= jt) {  // rows s, contraction over t
-                        const int row = 32 * jt + paired_row(lane, hh);
-                        const Planes<NP> qf = cols_at<typename Cf::KRow, NP, G, DK>(L.q, 32 * js, wj, wh, lane);
-                        ak = product<LIM>(rows_at<typename Cf::MRow, NP, G, G>(L.p, row, 4 * js + g), qf, ak);
-                        ak = product<LIM>(rows_at<typename Cf::MRow, NP, G, G>(L.m, row, 4 * js + g), kf, ak);
-                    }
-                }
-                dk[x] = ak;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dq[x][e] += aq[e];
+                for (int n = 0; n < NP; ++n)
+                    *reinterpret_cast<uint2*>(L.square[is_p ? 0 : 1] + n * MSIZE + Cf::MRow::at(t, s >> 3) + (s & 7)) = w[n];
             }
         }
+        // the state's part, and its sums over the key dimensions
+        float qsum[NX];
 #pragma unroll
-        for (int i = 0; i < 8 * NJ; ++i) {
-            const float s = group_sum<16>(qsum[i]);
-            if (m == (i & 15)) L.red[wave][32 * (i >> 3) + 8 * g + (i & 7)] = s;
+        for (int x = 0; x < NX; ++x) {
+            const int t = 32 * (x >> 1) + paired_row(lane, x & 1);
+            const float gm = L.gam[t], rb = L.rest[t] * L.beta[t], sg = a.scale * gm;
+            float into = 0.f, from = 0.f;
+#pragma unroll
+            for (int d = 0; d < TD; ++d) {
+                const int tile = TD * wave + d;  // key dimensions 32 (tile / 2) + 8 g + 4 (tile % 2) + 0..3
+                float qv[4] = {0.f, 0.f, 0.f, 0.f}, kv[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int n = NP - 1; n >= 0; --n) {
+                    const int o = n * KSIZE + Cf::KRow::at(t, 4 * (tile >> 1) + g) + 4 * (tile & 1);
+                    const u32x2 wq = *reinterpret_cast<const u32x2*>(L.q + o), wk = *reinterpret_cast<const u32x2*>(L.k + o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        qv[e] += __uint_as_float((e & 1) ? wq[e >> 1] & 0xffff0000u : wq[e >> 1] << 16);
+                        kv[e] += __uint_as_float((e & 1) ? wk[e >> 1] & 0xffff0000u : wk[e >> 1] << 16);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float o = sg * os[d][x][e], v = gm * vs[d][x][e], u = rb * ed[d][x][e];
+                    from = fmaf(qv[e], o, fmaf(-kv[e], v, from));
+                    into = fmaf(kv[e], u, into);
+                    os[d][x][e] = o;      // dQ so far
+                    ed[d][x][e] = u - v;  // dK so far
+                }
+            }
+            along += into;
+            qsum[x] = from - into;
+        }
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+            qsum[x] += __shfl_xor(qsum[x], 16, 64);
+            qsum[x] += __shfl_xor(qsum[x], 32, 64);
+            if (g == 0) L.red[wave][32 * (x >> 1) + paired_row(lane, x & 1)] = qsum[x];
         }
         along = wave_sum(along);
         if (lane == 0) L.ds[wave] = along;
         __syncthreads();
+#pragma unroll
+        for (int js = 0; js < NJ; ++js)
+#pragma unroll
+            for (int d = 0; d < TD; ++d) {
+                const int tile = TD * wave + d;
+                const Planes<NP> kf = cols_at<typename Cf::KRow, NP, KSIZE>(L.k, 32 * js, tile >> 1, tile & 1, lane);
+                const Planes<NP> qf = cols_at<typename Cf::KRow, NP, KSIZE>(L.q, 32 * js, tile >> 1, tile & 1, lane);
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int jt = x >> 1, row = 32 * jt + paired_row(lane, x & 1);
+                    if (js <= jt) {  // columns t, contraction over s
+                        os[d][x] = product<LIM>(kf, rows_at<typename Cf::MRow, NP, MSIZE>(L.square[0], row, 4 * js + g), os[d][x]);
+                        ed[d][x] = product<LIM>(kf, rows_at<typename Cf::MRow, NP, MSIZE>(L.square[1], row, 4 * js + g), ed[d][x]);
+                    }
+                    if (js >= jt) {  // columns s, contraction over t
+                        ed[d][x] = product<LIM>(qf, cols_at<typename Cf::MRow, NP, MSIZE>(L.square[0], 32 * js, jt, x & 1, lane), ed[d][x]);
+                        ed[d][x] = product<LIM>(kf, cols_at<typename Cf::MRow, NP, MSIZE>(L.square[1], 32 * js, jt, x & 1, lane), ed[d][x]);
+                    }
+                }
+            }
+        if constexpr (SHARED)
+#pragma unroll
+            for (int d = 0; d < TD; ++d)
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dq[d][x][e] += os[d][x][e];
+                        dk[d][x][e] += ed[d][x][e];
+                    }
+        if (!SHARED || hv == r - 1) {
+#pragma unroll
+            for (int d = 0; d < TD; ++d) {
+                const int tile = TD * wave + d;
+                const size_t col = 32 * (tile >> 1) + 8 * g + 4 * (tile & 1);
+#pragma unroll
+                for (int x = 0; x < NX; ++x) {
+                    const int t = 32 * (x >> 1) + paired_row(lane, x & 1);
+                    if (t < rows) {
+                        put4(static_cast<E*>(a.dq) + (rq + t) * DK + col, SHARED ? dq[SHARED ? d : 0][SHARED ? x : 0] : os[d][x]);
+                        put4(static_cast<E*>(a.dk) + (rq + t) * DK + col, SHARED ? dk[SHARED ? d : 0][SHARED ? x : 0] : ed[d][x]);
+                    }
+                }
+            }
+        }
         if (wave == 0) {
             float x = 0.f, ds = 0.f;
             if (lane < G) {
@@ -798,19 +897,6 @@ __global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads)) void delta_grad_ker
             }
         }
     }
-    const int d = 32 * wj + paired_row(lane, wh);
-    E* dqp = static_cast<E*>(a.dq) + rq * DK + d;
-    E* dkp = static_cast<E*>(a.dk) + rq * DK + d;
-#pragma unroll
-    for (int x = 0; x < 2 * NJ; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = 32 * (x >> 1) + 8 * g + 4 * (x & 1) + e;
-            if (t < rows) {
-                dqp[size_t(t) * DK] = from_f<E>(dq[x][e]);
-                dkp[size_t(t) * DK] = from_f<E>(dk[x][e]);
-            }
-        }
 }
 
 // ---------------------------------------------------------------------------- launches
@@ -819,7 +905,9 @@ template <typename E, int DK, int DV> void backward_d(const BackwardArgs& a, siz
     const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
     if constexpr (sizeof(E) == 2) delta_reverse_ahead_kernel<DK, DV><<<n, 64 * (W + 4), 0, st>>>(a);
     else delta_reverse_kernel<E, DK, W><<<n, Cfg<E, DK, W>::kThreads, 0, st>>>(a);
-    delta_grad_kernel<E, DK, DV><<<unsigned(slots * a.Hk), GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
+    const unsigned groups = unsigned(slots * a.Hk);
+    if (a.H > a.Hk) delta_grad_kernel<E, DK, DV, true><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
+    else delta_grad_kernel<E, DK, DV, false><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
 }
 template <typename E, int DK> void backward_k(const BackwardArgs& a, size_t slots, hipStream_t st) {
     if (a.dv == 32) backward_d<E, DK, 32>(a, slots, st);
