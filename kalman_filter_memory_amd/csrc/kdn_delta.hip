@@ -273,16 +273,16 @@ template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hi
 // ---------------------------------------------------------------------- bfloat16 inputs
 // The same recurrence with everything a chunk needs prepared further ahead, one barrier
 // per chunk and the rows copied straight into LDS.  While the recurrence is at chunk c,
-//   helper 3       copies chunk c + 4 (rows behind the sequence's last: that row again;
+//   helper 3       copies chunk c + 3 (rows behind the sequence's last: that row again;
 //                  beta 0 keeps them out of the state), and sums the decays of chunk c + 3
 //   helper 2       forms P of chunk c + 1
 //   helpers 0, 1   form the triangular system of chunk c + 2, and invert that of c + 1,
 //                  taking turns (a chunk stays with one of them)
 template <int DK, int DV, bool KEEP> struct AheadLds {
     static constexpr int W = DV == 32 ? 2 : 4, COLS = 16 * W;
-    bf16_t k[5][C * DK];
-    bf16_t q[KEEP ? 1 : 5][KEEP ? 8 : C * DK];
-    bf16_t v[5][C * COLS];
+    bf16_t k[4][C * DK];
+    bf16_t q[KEEP ? 1 : 4][KEEP ? 8 : C * DK];
+    bf16_t v[4][C * COLS];
     bf16_t t[2][3 * C * C];
     bf16_t p[KEEP ? 1 : 2][KEEP ? 8 : 2 * C * C];
     float a[2][C * kLdA];
@@ -322,11 +322,13 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + col0;
             const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), lv = lds_address(L.v);
             float g = 0.f, be = 0.f;
-            auto fetch = [&](int c, int s) {  // the gates and rows of chunk c
+            auto gates = [&](int c) {
                 const int t = c * C + (lane & 31);
                 g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
                 be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
-                const int rows = sq.len - c * C;
+            };
+            auto copy = [&](int c) {
+                const int rows = sq.len - c * C, s = c & 3;
                 copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
                 if constexpr (!KEEP) copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
                 copy_rows<COLS, true>(v + size_t(c) * (C * DV), DV, rows, lv + s * (C * COLS * 2), lane);
@@ -343,40 +345,40 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
                 }
             };
             if (nc > 0) {
-                fetch(0, 0);
+                gates(0);
+                copy(0);
                 sums(0);
             }
-            if (nc > 1) fetch(1, 1);
+            if (nc > 1) gates(1);
             copies_done<0>();
             sync_lds();
-            int s = 2;
             for (int c = -2; c < nc; ++c) {
-                copies_done<0>();  // chunk c + 3's rows (they had an interval)
-                if (c + 3 < nc) sums(c + 3);
-                if (c + 4 < nc) fetch(c + 4, s);
-                s = s == 4 ? 0 : s + 1;
+                if (c + 3 < nc) {
+                    sums(c + 3);
+                    if (c + 4 < nc) gates(c + 4);
+                    copy(c + 3);
+                }
+                copies_done<0>();
                 sync_lds();
             }
         } else if (hw == 2) {
             sync_lds();
-            int s = 4;  // where chunk c + 1 is
             for (int c = -2; c < nc; ++c) {
+                const int n = c + 1;
                 if constexpr (!KEEP)
-                    if (c >= -1 && c + 1 < nc)
-                        readout_of<Cf, false, 2>(L.q[s], L.k[s], L.G[(c + 1) & 3], a.scale, C, L.p[(c + 1) & 1], lane);
-                s = s == 4 ? 0 : s + 1;
+                    if (c >= -1 && n < nc)
+                        readout_of<Cf, false, 2>(L.q[n & 3], L.k[n & 3], L.G[n & 3], a.scale, C, L.p[n & 1], lane);
                 sync_lds();
             }
         } else {
             sync_lds();
-            int s = 0;  // where chunk c + 2 is
             for (int c = -2; c < nc; ++c) {
+                const int n = c + 2;
                 if ((c & 1) == hw) {
-                    if (c + 2 < nc) system_of<Cf, false>(L.k[s], L.G[(c + 2) & 3], L.beta[(c + 2) & 3], L.a[hw], lane);
+                    if (n < nc) system_of<Cf, false>(L.k[n & 3], L.G[n & 3], L.beta[n & 3], L.a[hw], lane);
                 } else if (c >= -1 && c + 1 < nc) {
                     invert<false>(L.a[hw], L.tmp[hw], L.t[(c + 1) & 1], lane);
                 }
-                s = s == 4 ? 0 : s + 1;
                 sync_lds();
             }
         }
@@ -424,10 +426,9 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
             for (int x = 0; x < 2; ++x) kf[x][j] = row_frag<Cf>(L.k[s], x, j, lane);
     };
-    int s = 0;
     if (nc > 0) fetch(0);
     for (int c = 0; c < nc; ++c) {
-        const int sg = c & 3;
+        const int s = c & 3;
         if constexpr (KEEP) {
             if (c % a.group == 0)
                 keep_state<bf16_t, KS>(
@@ -443,11 +444,11 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
-            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
+            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
             vw[x] = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
             ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
         }
-        const float last = L.gam[sg][C - 1];
+        const float last = L.gam[s][C - 1];
         if constexpr (!KEEP)
 #pragma unroll
             for (int j = 0; j < KS; ++j)
@@ -501,8 +502,8 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
-            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[sg][t]);
-            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[sg][t]);
+            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[s][t]);
+            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
         }
         // E = T R, beside the rest of Q S
         floatx4 ee[2];
@@ -535,8 +536,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
             for (int e = 0; e < 4; ++e) left[x][e] = KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
         if constexpr (!KEEP) lu = split8<2>(u);
-        s = s == 4 ? 0 : s + 1;
-        if (c + 1 < nc) fetch(s);
+        if (c + 1 < nc) fetch((c + 1) & 3);
         sync_lds();
     }
     if (nc > 0) results(nc - 1, sq.len - (nc - 1) * C);
