@@ -605,8 +605,10 @@ typedef struct {
 } kdn_delta_desc;
 
 /* Bytes of workspace kdn_gated_delta needs (0 if the descriptor is invalid; 16:
- * none, ws may be NULL).  Host-only. */
-size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc *d);
+ * none, ws may be NULL).  Few heads over long sequences are cut into segments whose
+ * maps it holds (the same recurrence, bracketed otherwise).  packed: whether
+ * cu_seqlens will be given.  Host-only. */
+size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc *d, int32_t packed);
 
 /* The recurrence over all tokens from S0 (NULL: zeros).  S_T: NULL or the last
  * states (S0 for a sequence without tokens), may be S0's buffer; o must not alias

@@ -198,7 +198,7 @@ def load_library(path: str = LIB_PATH):
     lib.kdn_gated_scan_backward.argtypes = [G] + [P] * 9 + [S, P]
     lib.kdn_gated_scan_step.argtypes = [G] + [P] * 4 + [ctypes.c_int32, P, P]
     E = ctypes.POINTER(KdnDeltaDesc)
-    lib.kdn_gated_delta_workspace_bytes.argtypes = [E]
+    lib.kdn_gated_delta_workspace_bytes.argtypes = [E, ctypes.c_int32]
     lib.kdn_gated_delta_workspace_bytes.restype = S
     lib.kdn_gated_delta.argtypes = [E] + [P] * 10 + [S, P]
     lib.kdn_gated_delta_backward_workspace_bytes.argtypes = [E, ctypes.c_int32]
@@ -1051,7 +1051,8 @@ def _gated_delta(q, k, v, g, beta, cu_seqlens, S0, scale, out):
         _tensors(("q", q), ("o", o), ("S_T", S_T))
         _shaped("o", o, v.dtype, v.shape)
         _shaped("S_T", S_T, torch.float32, states)
-    need = load_library().kdn_gated_delta_workspace_bytes(ctypes.byref(d))
+    need = load_library().kdn_gated_delta_workspace_bytes(ctypes.byref(d),
+                                                          int(cu_seqlens is not None))
     ws = _empty((need,), torch.uint8, dev) if need > 16 else None
     _launch("kdn_gated_delta", dev, ctypes.byref(d), _ptr(cu_seqlens), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(S0), o.data_ptr(), _ptr(S_T),

@@ -195,6 +195,18 @@ __device__ __forceinline__ Seq sequence(const int32_t* cu, int b, int h, int H, 
     return Seq{size_t(hk) * T + s, size_t(h) * T + s, s, e - s};
 }
 
+// Cuts segment `seg` of `segs` out of a sequence (whole groups of `group` chunks; those at
+// the end may be empty).  Returns its first chunk.
+__device__ __forceinline__ int cut_segment(Seq& sq, int seg, int segs, int group) {
+    if (segs <= 1) return 0;
+    const int all = (sq.len + C * group - 1) / (C * group), per = (all + segs - 1) / segs * group;
+    const int c0 = min(seg * per, all * group);
+    sq.rq += size_t(c0) * C;
+    sq.rv += size_t(c0) * C;
+    sq.len = max(0, min(sq.len - c0 * C, per * C));
+    return c0;
+}
+
 // Sums G of the log2 decays up to each token of a chunk, as hi + lo: differences of two
 // sums are then as exact as the decays between the two tokens, also behind a strong decay
 // (float32 sums alone would leave 2^-24 |G| in every later ratio).  A decay below 2^-160
@@ -556,6 +568,24 @@ template <int KS> __device__ __forceinline__ void store_state(const floatx4* st,
     for (int j = 0; j < KS; ++j) {
         *reinterpret_cast<floatx4*>(p + 32 * j) = st[2 * j];
         *reinterpret_cast<floatx4*>(p + 32 * j + 4) = st[2 * j + 1];
+    }
+}
+
+// columns col .. of the unit matrix as states: this lane's column, eight key dimensions a step
+template <int KS> __device__ __forceinline__ void unit_state(floatx4 (&st)[2 * KS], int col, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2 * KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[i][e] = 32 * (i >> 1) + 8 * (lane >> 4) + 4 * (i & 1) + e == col ? 1.f : 0.f;
+}
+// sixteen columns from col0 on of a map M [d_k][d_k], row by row
+template <int KS> __device__ __forceinline__ void store_map(const floatx4 (&st)[2 * KS], float* M, int col0, int lane) {
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+        const Planes<3> x = state_planes<2 * KS>(st, j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            put4(M + (32 * j + paired_row(lane, h)) * (32 * KS) + col0 + 4 * (lane >> 4), turned(x, unit(lane, h)));
     }
 }
 

@@ -1,6 +1,8 @@
 // kdn_delta.hip -- the gated delta rule over a sequence,
 //   S_t = e^g_t S_{t-1} + beta_t (v_t - e^g_t S_{t-1} k_t) k_t^T,   o_t = scale S_t q_t,
 // and one token of it on a cache of states (the mathematics of a chunk: kdn_delta.h).
+#include <algorithm>
+
 #include "kdn_delta.h"
 #include "kdn_delta_launch.h"
 
@@ -15,14 +17,17 @@ namespace {
 // alone, in registers; the results of one product are the operands of the next without
 // any exchange (paired_row).  Four more waves load the chunks into LDS and prepare T and
 // P a chunk ahead, which do not depend on the state.
-// KEEP: instead of o, the corrections E and the states that the backward pass needs.
-template <typename E, int DK, int W, bool KEEP> struct ForwardLds {
+// KEEP: instead of o, the corrections E and the states that the backward pass needs.  MAPS:
+// nothing but the state behind a segment, from the state in front of it or, in the
+// workgroups behind those, from the unit matrix with v = 0.
+enum Mode { READ = 0, KEEP = 1, MAPS = 2 };
+template <typename E, int DK, int W, int MODE> struct ForwardLds {
     using Cf = Cfg<E, DK, W>;
     bf16_t k[2][Cf::NP * C * DK];
-    bf16_t q[KEEP ? 1 : 2][KEEP ? 8 : Cf::NP * C * DK];
+    bf16_t q[MODE ? 1 : 2][MODE ? 8 : Cf::NP * C * DK];
     E v[2][C * Cf::LDV];
     bf16_t t[2][3 * C * C];
-    bf16_t p[KEEP ? 1 : 2][KEEP ? 8 : Cf::PP * C * C];
+    bf16_t p[MODE ? 1 : 2][MODE ? 8 : Cf::PP * C * C];
     float a[C * kLdA];
     float tmp[32 * kLdT];
     float gam[2][C], rest[2][C], beta[2][C];
@@ -30,29 +35,83 @@ template <typename E, int DK, int W, bool KEEP> struct ForwardLds {
     float gb[C];  // of the wave that inverts, of the one that prepares P
 };
 
-template <typename E, int DK, int W, bool KEEP>
+// What a workgroup takes: columns `slice` of a head's state (or, unit, of the unit matrix)
+// through segment seg of a sequence.
+struct Where {
+    int slice, h, b, seg;
+    bool unit;
+    size_t bh;  // of all heads
+    size_t heads;
+};
+template <int MODE> __device__ __forceinline__ Where where(const ForwardArgs& a, unsigned id, unsigned slices, unsigned dk) {
+    Where w{};
+    w.heads = size_t(a.B) * a.H;
+    if constexpr (MODE == MAPS) {
+        // segments 0 .. segs - 2 of the values, then 1 .. segs - 2 of the unit matrix
+        const unsigned first = unsigned(w.heads) * slices * unsigned(a.segs - 1);
+        w.unit = id >= first;
+        if (w.unit) {
+            id -= first;
+            slices = slices * dk / unsigned(a.dv);
+        }
+    }
+    w.slice = int(id % slices);
+    id /= slices;
+    w.h = int(id % unsigned(a.H));
+    id /= unsigned(a.H);
+    w.b = int(id % unsigned(a.B));
+    w.seg = int(id / unsigned(a.B)) + (w.unit ? 1 : 0);
+    w.bh = size_t(w.b) * a.H + w.h;
+    return w;
+}
+template <int MODE, int KS>
+__device__ __forceinline__ void state_in(const ForwardArgs& a, const Where& w, floatx4 (&st)[2 * KS], int col, int lane) {
+    const size_t size = size_t(a.dv) * (32 * KS);
+    // (segment 0 starts from its own copy: S_T may be S0's buffer)
+    const float* S = MODE != MAPS && a.segs > 1 ? a.starts + (w.seg * w.heads) * size : w.seg == 0 ? a.S0 : nullptr;
+    if (w.unit) {
+        unit_state<KS>(st, col, lane);
+    } else if (S != nullptr) {
+        load_state<KS>(st, S + w.bh * size, col, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (MODE == MAPS && w.seg == 0) store_state<KS>(st, a.starts + w.bh * size, col, lane);
+}
+template <int MODE, int KS>
+__device__ __forceinline__ void state_out(const ForwardArgs& a, const Where& w, const floatx4 (&st)[2 * KS], int col0, int lane) {
+    const size_t size = size_t(a.dv) * (32 * KS);
+    const int col = col0 + (lane & 15);
+    if constexpr (MODE == MAPS) {
+        if (w.unit) store_map<KS>(st, a.maps + ((w.seg - 1) * w.heads + w.bh) * size_t(32 * KS) * (32 * KS), col0, lane);
+        else store_state<KS>(st, a.starts + ((w.seg + 1) * w.heads + w.bh) * size, col, lane);
+    } else {
+        if (a.S_T != nullptr && w.seg == max(a.segs, 1) - 1) store_state<KS>(st, a.S_T + w.bh * size, col, lane);
+    }
+}
+
+template <typename E, int DK, int W, int MODE>
 __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kernel(ForwardArgs a) {
     using Cf = Cfg<E, DK, W>;
     constexpr int NP = Cf::NP, PP = Cf::PP, KT = Cf::KT, KS = Cf::KS, HT = 64 * Cf::NH;
-    __shared__ __align__(16) ForwardLds<E, DK, W, KEEP> L;
+    __shared__ __align__(16) ForwardLds<E, DK, W, MODE> L;
 
-    const unsigned slices = unsigned(a.dv) / Cf::COLS;
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
-    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), unsigned(a.dv) / Cf::COLS, DK);
+    const int h = at.h, b = at.b, col0 = at.slice * Cf::COLS;
+    Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int start = sq.start, c0 = cut_segment(sq, at.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int col0 = slice * Cf::COLS;
-    const size_t state = (size_t(b) * a.H + h) * size_t(a.dv) * DK;
 
     const E* q = static_cast<const E*>(a.q) + sq.rq * DK;
     const E* k = static_cast<const E*>(a.k) + sq.rq * DK;
-    const E* v = static_cast<const E*>(a.v) + sq.rv * a.dv + col0;
+    const E* v = static_cast<const E*>(a.v) + sq.rv * a.dv + (at.unit ? 0 : col0);
 
     // zeros: the halves of T and P that no wave writes
     for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += Cf::kThreads)
         reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
-    if constexpr (!KEEP)
+    if constexpr (MODE == READ)
         for (unsigned i = threadIdx.x; i < 2 * PP * C * C / 8; i += Cf::kThreads)
             reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
     sync_lds();
@@ -66,7 +125,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
         auto load = [&](int c) {
             const int t0 = c * C, rows = sq.len - t0;
             sk.load(k + size_t(t0) * DK, DK, rows, ht);
-            if constexpr (!KEEP) sq_.load(q + size_t(t0) * DK, DK, rows, ht);
+            if constexpr (MODE == READ) sq_.load(q + size_t(t0) * DK, DK, rows, ht);
             sv.load(v + size_t(t0) * a.dv, a.dv, rows, ht);
         };
         auto gates = [&](int c) {  // of chunk c, token lane % 32
@@ -82,7 +141,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
                 for (int n = 0; n < NP; ++n)
                     *reinterpret_cast<bf16x8*>(L.k[s] + n * C * DK + Cf::Tile::at(row, p)) = x.p[n];
             });
-            if constexpr (!KEEP)
+            if constexpr (MODE == READ)
                 sq_.each(ht, [&](const Raw8<E>& r, int row, int p) {
                     const auto x = planes_of<E>(r);
 #pragma unroll
@@ -115,7 +174,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
                     L.rest[s][lane] = decay_between(last, G);
                     L.beta[s][lane] = be;
                 }
-                if constexpr (!KEEP) {
+                if constexpr (MODE == READ) {
                     wave_lds_fence();
                     readout_of<Cf, false, PP>(L.q[s], L.k[s], L.G[1], a.scale, C, L.p[s], lane);
                 }
@@ -150,18 +209,14 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
     // --------------------------------------------------------------------- recurrence
     const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
     floatx4 st[KT];
-    if (a.S0 != nullptr) {
-        load_state<KS>(st, a.S0 + state, col, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const size_t groups = KEEP ? group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) : 0;
+    state_in<MODE, KS>(a, at, st, col, lane);
+    const size_t groups =
+        MODE == KEEP ? group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group : 0;
     sync_lds();
     sync_lds();
     for (int c = 0; c < nc; ++c) {
         const int s = c & 1;
-        if constexpr (KEEP) {
+        if constexpr (MODE == KEEP) {
             if (c % a.group == 0)
                 keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK,
                                   col0 + 16 * wave, lane);
@@ -175,7 +230,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
             const Planes<3> sp = state_planes<KT>(st, j);
 #pragma unroll
             for (int x = 0; x < 2; ++x) ks[x] = product<2>(row_frag<Cf>(L.k[s], x, j, lane), sp, ks[x]);
-            if constexpr (!KEEP)
+            if constexpr (MODE == READ)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) qs[x] = product<PP - 1>(row_frag<Cf>(L.q[s], x, j, lane), sp, qs[x]);
         }
@@ -198,7 +253,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
                 for (int e = 0; e < 4; ++e) vv[e] = L.v[s][(t + e) * Cf::LDV + 16 * wave + m];
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * x + e] = vv[e] - gam[x][e] * ks[x][e];
+            for (int e = 0; e < 4; ++e) f[4 * x + e] = (at.unit ? 0.f : vv[e]) - gam[x][e] * ks[x][e];
         }
         const Planes<3> rp = split8<3>(f);
         floatx4 ee[2];
@@ -222,7 +277,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
             st[i] = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), up, w);
         }
         const int rows = sq.len - c * C;
-        if constexpr (KEEP) {
+        if constexpr (MODE == KEEP) {
             E* out = static_cast<E*>(a.keep_E) + (sq.rv + size_t(c) * C) * a.dv + col;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -231,7 +286,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
                     const int t = 8 * g + 4 * x + e;
                     if (t < rows) out[size_t(t) * a.dv] = from_f<E>(ee[x][e]);
                 }
-        } else {
+        } else if constexpr (MODE == READ) {
             const Planes<PP> uo = split8<PP>(u);
             E* out = static_cast<E*>(a.o) + (sq.rv + size_t(c) * C) * a.dv + col;
 #pragma unroll
@@ -250,24 +305,30 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
         sync_lds();
         sync_lds();
     }
-    if (a.S_T != nullptr) store_state<KS>(st, a.S_T + state, col, lane);
+    state_out<MODE, KS>(a, at, st, col0 + 16 * wave, lane);
 }
 
-template <typename E, int DK, int W>
-void forward_dw(const ForwardArgs& a, bool keep, hipStream_t st) {
-    const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(a.dv / (16 * W));
-    constexpr int threads = Cfg<E, DK, W>::kThreads;
-    if (keep) delta_forward_kernel<E, DK, W, true><<<n, threads, 0, st>>>(a);
-    else delta_forward_kernel<E, DK, W, false><<<n, threads, 0, st>>>(a);
+unsigned workgroups(const ForwardArgs& a, int mode, int dk, int cols) {
+    const unsigned heads = unsigned(a.B) * unsigned(a.H), slices = unsigned(a.dv / cols);
+    if (mode == MAPS) return heads * (slices * unsigned(a.segs - 1) + unsigned(dk / cols) * unsigned(a.segs - 2));
+    return heads * slices * unsigned(std::max(a.segs, 1));
 }
-template <typename E, int DK> void forward_d(const ForwardArgs& a, bool keep, hipStream_t st) {
-    if (a.dv == 32) forward_dw<E, DK, 2>(a, keep, st);
-    else forward_dw<E, DK, 4>(a, keep, st);
+template <int DK, int W> void forward_dw(const ForwardArgs& a, int mode, hipStream_t st) {
+    const unsigned n = workgroups(a, mode, DK, 16 * W);
+    constexpr int threads = Cfg<float, DK, W>::kThreads;
+    if (mode == KEEP) delta_forward_kernel<float, DK, W, KEEP><<<n, threads, 0, st>>>(a);
+    else if (mode == MAPS) delta_forward_kernel<float, DK, W, MAPS><<<n, threads, 0, st>>>(a);
+    else delta_forward_kernel<float, DK, W, READ><<<n, threads, 0, st>>>(a);
 }
-template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hipStream_t st) {
-    if (dk == 32) forward_d<E, 32>(a, keep, st);
-    else if (dk == 64) forward_d<E, 64>(a, keep, st);
-    else forward_d<E, 128>(a, keep, st);
+template <int DK> void forward_d(const ForwardArgs& a, int mode, hipStream_t st) {
+    // (two waves where a slice of four would be wider than d_v, or than the unit matrix)
+    if (a.dv == 32 || DK == 32) forward_dw<DK, 2>(a, mode, st);
+    else forward_dw<DK, 4>(a, mode, st);
+}
+void forward_f32(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
+    if (dk == 32) forward_d<32>(a, mode, st);
+    else if (dk == 64) forward_d<64>(a, mode, st);
+    else forward_d<128>(a, mode, st);
 }
 
 // ---------------------------------------------------------------------- bfloat16 inputs
@@ -278,39 +339,37 @@ template <typename E> void forward_e(const ForwardArgs& a, int dk, bool keep, hi
 //   helper 2       forms P of chunk c + 1
 //   helpers 0, 1   form the triangular system of chunk c + 2, and invert that of c + 1,
 //                  taking turns (a chunk stays with one of them)
-template <int DK, int DV, bool KEEP> struct AheadLds {
-    static constexpr int W = DV == 32 ? 2 : 4, COLS = 16 * W;
+template <int DK, int DV, int MODE> struct AheadLds {
+    static constexpr int W = DV == 32 || DK == 32 ? 2 : 4, COLS = 16 * W;
     bf16_t k[4][C * DK];
-    bf16_t q[KEEP ? 1 : 4][KEEP ? 8 : C * DK];
+    bf16_t q[MODE ? 1 : 4][MODE ? 8 : C * DK];
     bf16_t v[4][C * COLS];
     bf16_t t[2][3 * C * C];
-    bf16_t p[KEEP ? 1 : 2][KEEP ? 8 : 2 * C * C];
+    bf16_t p[MODE ? 1 : 2][MODE ? 8 : 2 * C * C];
     float a[2][C * kLdA];
     float tmp[2][32 * kLdT];
     float gam[4][C], rest[4][C], beta[4][C];
     LogSum G[4][C];
 };
 
-template <int DK, int DV, bool KEEP>
-__global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
-    using Lds = AheadLds<DK, DV, KEEP>;
+template <int DK, int DV, int MODE>
+__global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
+    using Lds = AheadLds<DK, DV, MODE>;
     constexpr int W = Lds::W, COLS = Lds::COLS;
     using Cf = Cfg<bf16_t, DK, W>;
     constexpr int KT = Cf::KT, KS = Cf::KS;
     __shared__ __align__(16) Lds L;
 
-    constexpr unsigned slices = DV / COLS;
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
-    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), DV / COLS, DK);
+    const int h = at.h, b = at.b, col0 = at.slice * COLS;
+    Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int start = sq.start, c0 = cut_segment(sq, at.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int col0 = slice * COLS;
-    const size_t state = (size_t(b) * a.H + h) * size_t(DV) * DK;
 
     for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += 64 * (W + 4))
         reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
-    if constexpr (!KEEP)
+    if constexpr (MODE == READ)
         for (unsigned i = threadIdx.x; i < 2 * 2 * C * C / 8; i += 64 * (W + 4))
             reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
 
@@ -319,7 +378,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
         if (hw == 3) {
             const bf16_t* q = static_cast<const bf16_t*>(a.q) + sq.rq * DK;
             const bf16_t* k = static_cast<const bf16_t*>(a.k) + sq.rq * DK;
-            const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + col0;
+            const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + (at.unit ? 0 : col0);
             const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), lv = lds_address(L.v);
             float g = 0.f, be = 0.f;
             auto gates = [&](int c) {
@@ -330,7 +389,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             auto copy = [&](int c) {
                 const int rows = sq.len - c * C, s = c & 3;
                 copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
-                if constexpr (!KEEP) copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
+                if constexpr (MODE == READ) copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
                 copy_rows<COLS, true>(v + size_t(c) * (C * DV), DV, rows, lv + s * (C * COLS * 2), lane);
             };
             auto sums = [&](int c) {
@@ -365,7 +424,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             sync_lds();
             for (int c = -2; c < nc; ++c) {
                 const int n = c + 1;
-                if constexpr (!KEEP)
+                if constexpr (MODE == READ)
                     if (c >= -1 && n < nc)
                         readout_of<Cf, false, 2>(L.q[n & 3], L.k[n & 3], L.G[n & 3], a.scale, C, L.p[n & 1], lane);
                 sync_lds();
@@ -388,14 +447,10 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
     // --------------------------------------------------------------------- recurrence
     const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
     floatx4 st[KT];
-    if (a.S0 != nullptr) {
-        load_state<KS>(st, a.S0 + state, col, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const size_t groups = KEEP ? group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) : 0;
-    bf16_t* out = static_cast<bf16_t*>(KEEP ? a.keep_E : a.o) + sq.rv * DV + col0 + 16 * wave + 4 * g;
+    state_in<MODE, KS>(a, at, st, col, lane);
+    const size_t groups =
+        MODE == KEEP ? group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group : 0;
+    bf16_t* out = static_cast<bf16_t*>(MODE == KEEP ? a.keep_E : a.o) + sq.rv * DV + col0 + 16 * wave + 4 * g;
     sync_lds();
     sync_lds();
     sync_lds();
@@ -412,7 +467,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
     auto results = [&](int c, int rows) {
         floatx4 o[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) o[x] = KEEP ? left[x] : product<1>(lp[x], lu, left[x]);
+        for (int x = 0; x < 2; ++x) o[x] = MODE == KEEP ? left[x] : product<1>(lp[x], lu, left[x]);
         const Planes<1> r = {{pack8(o[0], o[1])}};
         bf16_t* p = out + size_t(c) * (C * DV);
 #pragma unroll
@@ -429,7 +484,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
     if (nc > 0) fetch(0);
     for (int c = 0; c < nc; ++c) {
         const int s = c & 3;
-        if constexpr (KEEP) {
+        if constexpr (MODE == KEEP) {
             if (c % a.group == 0)
                 keep_state<bf16_t, KS>(
                     st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK,
@@ -449,7 +504,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
             ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
         }
         const float last = L.gam[s][C - 1];
-        if constexpr (!KEEP)
+        if constexpr (MODE == READ)
 #pragma unroll
             for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -462,7 +517,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
             for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j].p[0], st[2 * j + x]);
         }
-        if (c > 0) results(c - 1, C);
+        if (MODE != MAPS && c > 0) results(c - 1, C);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
             sp[j].p[1] = pack8(r1[2 * j], r1[2 * j + 1]);
@@ -486,7 +541,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
         for (int x = 0; x < 2; ++x) tf[x] = square_frag<3>(L.t[c & 1], x, lane);
         // R = V - gamma K S, beside Q S
-        if constexpr (!KEEP)
+        if constexpr (MODE == READ)
 #pragma unroll
             for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -495,7 +550,8 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * x + e] = bf2f(static_cast<bf16_t>(vw[x][e])) - gam[x][e] * ks[x][e];
+            for (int e = 0; e < 4; ++e)
+                f[4 * x + e] = (at.unit ? 0.f : bf2f(static_cast<bf16_t>(vw[x][e]))) - gam[x][e] * ks[x][e];
         const Planes<3> rp = split8<3>(f);
 #pragma unroll
         for (int i = 0; i < KT; ++i) kt[i] = col_frag<Cf>(L.k[s], i / 2, i % 2, lane);
@@ -509,7 +565,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
         floatx4 ee[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) ee[x] = product<2>(tf[x], rp, floatx4{0.f, 0.f, 0.f, 0.f});
-        if constexpr (!KEEP) {
+        if constexpr (MODE == READ) {
 #pragma unroll
             for (int j = 0; j < KS; ++j)
 #pragma unroll
@@ -534,30 +590,66 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, KEEP>::W + 4)) void delta_ah
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) left[x][e] = KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
-        if constexpr (!KEEP) lu = split8<2>(u);
+            for (int e = 0; e < 4; ++e) left[x][e] = MODE == KEEP ? ee[x][e] : a.scale * gam[x][e] * qs[x][e];
+        if constexpr (MODE == READ) lu = split8<2>(u);
         if (c + 1 < nc) fetch((c + 1) & 3);
         sync_lds();
     }
-    if (nc > 0) results(nc - 1, sq.len - (nc - 1) * C);
-    if (a.S_T != nullptr) store_state<KS>(st, a.S_T + state, col, lane);
+    if (MODE != MAPS && nc > 0) results(nc - 1, sq.len - (nc - 1) * C);
+    state_out<MODE, KS>(a, at, st, col0 + 16 * wave, lane);
 }
 
-template <int DK, int DV> void ahead_go(const ForwardArgs& a, bool keep, hipStream_t st) {
-    constexpr int W = AheadLds<DK, DV, false>::W;
-    const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
-    if (keep) delta_ahead_kernel<DK, DV, true><<<n, 64 * (W + 4), 0, st>>>(a);
-    else delta_ahead_kernel<DK, DV, false><<<n, 64 * (W + 4), 0, st>>>(a);
+template <int DK, int DV> void ahead_go(const ForwardArgs& a, int mode, hipStream_t st) {
+    constexpr int W = AheadLds<DK, DV, READ>::W, threads = 64 * (W + 4);
+    const unsigned n = workgroups(a, mode, DK, 16 * W);
+    if (mode == KEEP) delta_ahead_kernel<DK, DV, KEEP><<<n, threads, 0, st>>>(a);
+    else if (mode == MAPS) delta_ahead_kernel<DK, DV, MAPS><<<n, threads, 0, st>>>(a);
+    else delta_ahead_kernel<DK, DV, READ><<<n, threads, 0, st>>>(a);
 }
-template <int DK> void ahead_dv(const ForwardArgs& a, bool keep, hipStream_t st) {
-    if (a.dv == 32) ahead_go<DK, 32>(a, keep, st);
-    else if (a.dv == 64) ahead_go<DK, 64>(a, keep, st);
-    else ahead_go<DK, 128>(a, keep, st);
+template <int DK> void ahead_dv(const ForwardArgs& a, int mode, hipStream_t st) {
+    if (a.dv == 32) ahead_go<DK, 32>(a, mode, st);
+    else if (a.dv == 64) ahead_go<DK, 64>(a, mode, st);
+    else ahead_go<DK, 128>(a, mode, st);
 }
-void forward_bf16(const ForwardArgs& a, int dk, bool keep, hipStream_t st) {
-    if (dk == 32) ahead_dv<32>(a, keep, st);
-    else if (dk == 64) ahead_dv<64>(a, keep, st);
-    else ahead_dv<128>(a, keep, st);
+void forward_bf16(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
+    if (dk == 32) ahead_dv<32>(a, mode, st);
+    else if (dk == 64) ahead_dv<64>(a, mode, st);
+    else ahead_dv<128>(a, mode, st);
+}
+
+// ------------------------------------------------------------------- segments' states
+// starts[g + 1] <- M_g starts[g] + starts[g + 1] for g = 1 .. segs - 2 (starts[1] is there
+// already), 16 columns of a head's states per wave, in the order of the recurrence.  A step
+// takes about 4 us at d_k 128: a map's 64 KB on their way from memory, and their products.
+template <int DK>
+__global__ __launch_bounds__(256) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* starts) {
+    constexpr int KS = DK / 32;
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const int groups = (dv + 63) / 64;
+    const size_t bh = blockIdx.x / groups, size = size_t(dv) * DK;
+    const int col = (blockIdx.x % groups) * 64 + 16 * wave + (lane & 15);
+    if (col >= dv) return;
+    floatx4 st[2 * KS];
+    load_state<KS>(st, starts + (size_t(heads) + bh) * size, col, lane);
+    for (int s = 1; s < segs - 1; ++s) {
+        const float* M = maps + ((s - 1) * size_t(heads) + bh) * size_t(DK) * DK + 8 * (lane >> 4);
+        float* S = starts + ((s + 1) * size_t(heads) + bh) * size;
+        Planes<3> sp[KS];
+#pragma unroll
+        for (int j = 0; j < KS; ++j) sp[j] = state_planes<2 * KS>(st, j);
+        load_state<KS>(st, S, col, lane);
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+            const float* row = M + (32 * (i >> 1) + paired_row(lane, i & 1)) * DK;
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                float f[8];
+                load_vec<float, 8>(row + 32 * j, f);
+                st[i] = product<2>(split8<3>(f), sp[j], st[i]);
+            }
+        }
+        store_state<KS>(st, S, col, lane);
+    }
 }
 
 // ------------------------------------------------------------------------- one token
@@ -669,8 +761,56 @@ kdn_status check(const kdn_delta_desc* d, bool one_token) {
 }
 
 hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st) {
-    if (dtype == KDN_BF16) forward_bf16(a, dk, keep, st);
-    else forward_e<float>(a, dk, keep, st);
+    if (dtype == KDN_BF16) forward_bf16(a, dk, keep ? KEEP : READ, st);
+    else forward_f32(a, dk, keep ? KEEP : READ, st);
+    return hipGetLastError();
+}
+
+// The count is chosen by an estimate of the launches' rounds of 256 workgroups: a chunk of
+// 32 tokens takes 1.7 us with the read-out and 1.4 without (d 128, bfloat16), a step of the
+// composition 4 us, two more launches 8.
+Segments segments_of(const kdn_delta_desc* d, bool packed, int group) {
+    Segments s{};
+    s.count = 1;
+    s.total = 16;
+    const int64_t heads = int64_t(d->B) * d->H, cols = d->d_v == 32 || d->d_k == 32 ? 32 : 64;
+    const int64_t tokens = packed ? d->T / std::max(d->B, 1) : d->T, nc = (tokens + C - 1) / C;
+    const int64_t w = heads * (d->d_v / cols), wk = heads * (d->d_k / cols);
+    if (heads == 0 || w > 128 || nc < 16) return s;
+    auto rounds = [](int64_t n) { return double((n + 255) / 256); };
+    const double scale = 0.5 + d->d_k / 256.0;
+    double best = 0.8 * scale * 1.7 * nc * rounds(w);
+    for (int n = 2; n <= 64 && n * 4 <= nc; ++n) {
+        const int64_t per = ((nc + n - 1) / n + group - 1) / group * group;
+        const double t = scale * per * (1.4 * rounds(w * (n - 1) + wk * (n - 2)) + 1.7 * rounds(w * n)) + 4.0 * (n - 2) + 8.0;
+        if (t < best) {
+            best = t;
+            s.count = n;
+        }
+    }
+    if (s.count > 1) {
+        auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+        s.starts = 0;
+        s.maps = up(size_t(s.count) * heads * d->d_v * d->d_k * 4);
+        s.total = s.maps + up(size_t(s.count - 2) * heads * d->d_k * d->d_k * 4) + 16;
+    }
+    return s;
+}
+
+hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtype, int dk, hipStream_t st) {
+    a.segs = s.count;
+    if (s.count <= 1) return hipSuccess;
+    a.starts = reinterpret_cast<float*>(static_cast<char*>(ws) + s.starts);
+    a.maps = reinterpret_cast<float*>(static_cast<char*>(ws) + s.maps);
+    if (dtype == KDN_BF16) forward_bf16(a, dk, MAPS, st);
+    else forward_f32(a, dk, MAPS, st);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || s.count == 2) return e;
+    const int heads = a.B * a.H;
+    const unsigned n = unsigned(heads) * unsigned((a.dv + 63) / 64);
+    if (dk == 32) delta_compose_kernel<32><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
+    else if (dk == 64) delta_compose_kernel<64><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
+    else delta_compose_kernel<128><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
     return hipGetLastError();
 }
 
@@ -685,8 +825,9 @@ hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st) 
 
 extern "C" {
 
-size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc* d) {
-    return kdn::delta::check(d, false) == KDN_OK ? 16 : 0;
+size_t kdn_gated_delta_workspace_bytes(const kdn_delta_desc* d, int32_t packed) {
+    using namespace kdn::delta;
+    return check(d, false) == KDN_OK ? segments_of(d, packed != 0, 1).total : 0;
 }
 
 kdn_status kdn_gated_delta(const kdn_delta_desc* d, const int32_t* cu_seqlens, const void* q, const void* k, const void* v,
@@ -701,7 +842,9 @@ kdn_status kdn_gated_delta(const kdn_delta_desc* d, const int32_t* cu_seqlens, c
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (d->T == 0)
         return launch_states(size_t(d->B) * d->H * d->d_k * d->d_v, S0, S_T, st) == hipSuccess ? KDN_OK : KDN_ERR_HIP;
-    if (!q || !k || !v || !g || !beta || !o) return KDN_ERR_NULL;
+    const Segments s = segments_of(d, cu_seqlens != nullptr, 1);
+    if (!q || !k || !v || !g || !beta || !o || (s.count > 1 && !ws)) return KDN_ERR_NULL;
+    if (s.count > 1 && ws_bytes < s.total) return KDN_ERR_WORKSPACE;
     ForwardArgs a{};
     a.q = q;
     a.k = k;
@@ -719,6 +862,8 @@ kdn_status kdn_gated_delta(const kdn_delta_desc* d, const int32_t* cu_seqlens, c
     a.dv = d->d_v;
     a.scale = d->scale;
     a.gate_bf16 = d->gate_dtype == KDN_BF16;
+    a.group = 1;
+    if (launch_segments(a, s, ws, d->dtype, d->d_k, st) != hipSuccess) return KDN_ERR_HIP;
     return launch_forward(a, d->dtype, d->d_k, false, st) == hipSuccess ? KDN_OK : KDN_ERR_HIP;
 }
 

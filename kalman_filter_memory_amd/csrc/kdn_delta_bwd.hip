@@ -921,8 +921,9 @@ template <typename E> void backward_e(const BackwardArgs& a, int dk, size_t slot
 }
 
 struct Layout {
-    size_t E, S, D, part, total;
+    size_t E, S, D, part, segments, total;
     size_t rows, slots;
+    Segments seg;
 };
 Layout layout_of(const kdn_delta_desc* d, bool packed) {
     Layout l{};
@@ -934,7 +935,9 @@ Layout layout_of(const kdn_delta_desc* d, bool packed) {
     l.S = up(l.rows * d->d_v * e);
     l.D = l.S + up(l.slots * d->H * d->d_v * d->d_k * e);
     l.part = l.D + up(l.slots * d->H * d->d_v * d->d_k * e);
-    l.total = l.part + up(l.rows * (d->d_v / 16) * 4) + 16;
+    l.segments = l.part + up(l.rows * (d->d_v / 16) * 4);
+    l.seg = segments_of(d, packed, kept_chunks(d->dtype));
+    l.total = l.segments + l.seg.total;
     return l;
 }
 
@@ -996,6 +999,7 @@ kdn_status kdn_gated_delta_backward(const kdn_delta_desc* d, const int32_t* cu_s
     f.group = kept_chunks(d->dtype);
     f.scale = d->scale;
     f.gate_bf16 = d->gate_dtype == KDN_BF16;
+    if (launch_segments(f, l.seg, w + l.segments, d->dtype, d->d_k, st) != hipSuccess) return KDN_ERR_HIP;
     if (launch_forward(f, d->dtype, d->d_k, true, st) != hipSuccess) return KDN_ERR_HIP;
 
     BackwardArgs a{};

@@ -24,7 +24,10 @@ struct ForwardArgs {
     float* S_T;
     void *keep_E, *keep_S;  // for the backward pass
     int B, H, Hk, T, dv;
-    int group;  // chunks per kept state
+    int group;  // chunks per kept state (and a multiple of which a segment holds)
+    // segments of every sequence (see Segments); maps: this launch forms their maps
+    int segs;
+    float *starts, *maps;
     float scale;
     bool gate_bf16;
 };
@@ -36,6 +39,19 @@ inline size_t kept_slots(const int32_t* cu, int B, int T, int group) {
     const int per = 32 * group;
     return cu != nullptr ? size_t(T / per) + B + 1 : size_t(B) * ((T + per - 1) / per);
 }
+
+// Few heads over long sequences leave most of the CUs idle, so their chunks are cut into
+// `count` segments: a segment's tokens map the state in front of them affinely, S -> M S +
+// N (S [d_k, d_v]; N from the zero state, M from the unit matrix with v = 0), all maps but
+// the last segment's are formed at once, composed in order, and every segment then runs
+// from its own state.
+struct Segments {
+    int count;
+    size_t starts, maps, total;  // bytes: states in front of each segment, M of 1 .. count - 2
+};
+Segments segments_of(const kdn_delta_desc* d, bool packed, int group);
+// The states in front of all segments, in a.starts, from a.S0; sets a.segs and the pointers
+hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtype, int dk, hipStream_t st);
 
 kdn_status check(const kdn_delta_desc* d, bool one_token);
 hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st);

@@ -35,7 +35,8 @@ BAD = [
 @pytest.mark.parametrize("kw,code", BAD, ids=[str(k) for k, _ in BAD])
 def test_refuses_descriptors(lib, kw, code):
     d = ctypes.byref(_desc(**kw))
-    assert lib.kdn_gated_delta_workspace_bytes(d) == 0
+    for packed in (0, 1):
+        assert lib.kdn_gated_delta_workspace_bytes(d, packed) == 0
     assert lib.kdn_gated_delta(d, None, *([FAKE] * 9), 1 << 40, None) == code
     assert lib.kdn_gated_delta_step(d, *([FAKE] * 6), None, 0, FAKE, None) == code
     for packed in (0, 1):
@@ -45,14 +46,14 @@ def test_refuses_descriptors(lib, kw, code):
 
 def test_refuses_too_many_tokens(lib):
     d = ctypes.byref(_desc(T=(1 << 30) + 1))
-    assert lib.kdn_gated_delta_workspace_bytes(d) == 0
+    assert lib.kdn_gated_delta_workspace_bytes(d, 0) == 0
     assert lib.kdn_gated_delta(d, None, *([FAKE] * 9), 1 << 40, None) == 3
 
 
 def test_refuses_arguments(lib):
     d = ctypes.byref(_desc())
-    need = lib.kdn_gated_delta_workspace_bytes(d)
-    assert need >= 16
+    need = lib.kdn_gated_delta_workspace_bytes(d, 0)
+    assert need == 16  # none
     assert lib.kdn_gated_delta(None, None, *([FAKE] * 9), need, None) == 1
     for i in (0, 1, 2, 3, 4, 6):  # q, k, v, g, beta, o
         args = [FAKE] * 9

@@ -26,11 +26,12 @@ SHAPES = [
 IDS = ["-".join(map(str, s)) for s in SHAPES]
 
 
-def _compare(x, S0, o, S_T, scale=None):
+def _compare(x, S0, o, S_T, scale=None, times=1):
     q, k, v, g, beta = x
     scale = q.shape[-1] ** -0.5 if scale is None else scale
     want, last, kept = delta(q, k, v, g, beta, S0, scale)
     D, s = state_errors(q, k, v, g, beta, kept)
+    D = times * D
     assert o.dtype == v.dtype and o.shape == v.shape and S_T.dtype == torch.float32
     size = s + (v.double().norm(dim=-1).amax(-1) if v.shape[2] else 0)
     tol = D + 70 * U * s[..., None] + (2.0 ** -14 * 2 * size[..., None] if v.dtype == torch.bfloat16 else 0)
@@ -114,6 +115,36 @@ def test_wrong_offsets_stay_inside():
     kdn.gated_delta_varlen(*x, cu, S0, out=(o, S_T))
     whole = kdn.gated_delta(*(t[None] for t in x), S0[:1])
     assert torch.equal(o, whole[0][0]) and torch.equal(S_T[0], whole[1][0]) and torch.equal(S_T[1], S0[1])
+
+
+@pytest.mark.parametrize("shape", [
+    (1, 1, 1, 2100, 128, 128, "bf16", "f32"), (1, 2, 1, 1999, 64, 32, "bf16", "bf16"), (2, 1, 1, 1600, 32, 128, "f32", "f32"),
+    (1, 1, 1, 1700, 128, 64, "f32", "bf16"), (1, 3, 3, 2900, 32, 64, "bf16", "f32"), (1, 1, 1, 1537, 64, 64, "f32", "f32")])
+def test_few_heads_over_long_sequences(shape):
+    """Cut into segments (a workspace is asked for), also over the first state's own buffer.
+    The composition adds the maps' errors, which each are a state's: twice the bound."""
+    *x, S0 = inputs(*shape, seed=44)
+    B, H, Hk, T, dk, dv, dtype, gate = shape
+    code = {"f32": kdn.F32, "bf16": kdn.BF16}
+    d = kdn.make_delta_desc(B, H, Hk, T, dk, dv, code[dtype], code[gate])
+    assert kdn.load_library().kdn_gated_delta_workspace_bytes(ctypes.byref(d), 0) > 16
+    say(f"[gpu] gated_delta in segments {shape}")
+    o, S_T = kdn.gated_delta(*x, S0)
+    _compare(x, S0, o, S_T, times=2)
+    S, again = S0.clone(), torch.empty_like(o)
+    kdn.gated_delta(*x, S, out=(again, S))
+    assert torch.equal(again, o) and torch.equal(S, S_T)
+
+
+def test_long_packed_sequences_of_few_heads():
+    lengths = (1500, 3, 0, 1100, 33)
+    x, cu, S0 = _packed(lengths, 1, 1, 64, 64, "f32", "f32", 13)
+    o, S_T = kdn.gated_delta_varlen(*x, cu, S0)
+    at = 0
+    for i, n in enumerate(lengths):
+        part = [t[None, :, at:at + n].contiguous() for t in x]
+        _compare(part, S0[i:i + 1], o[None, :, at:at + n], S_T[i:i + 1], times=2)
+        at += n
 
 
 def test_no_tokens():

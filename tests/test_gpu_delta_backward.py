@@ -59,6 +59,14 @@ def test_matches_the_formula(shape, kind):
         assert torch.equal(got[n], again[n]), n
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1500, 64, 64, "f32", "f32"), (1, 2, 1, 1203, 128, 32, "bf16", "f32")])
+def test_few_heads_over_long_sequences(shape):
+    x, do, S0, dS_T = _all(shape, 52)
+    say(f"[gpu] gated_delta_backward in segments {shape}")
+    got = kdn.gated_delta_backward(*x, do, S0, dS_T)
+    _check(got, *rounding_bounds(*x, do, S0, dS_T, HALF[x[2].dtype]), x[2].dtype)
+
+
 def test_without_states_and_with_another_scale():
     x, do, S0, _ = _all((2, 2, 1, 70, 64, 64, "f32", "f32"), 6)
     zero = torch.zeros_like(S0)
