@@ -18,8 +18,8 @@ namespace {
 // any exchange (paired_row).  Four more waves load the chunks into LDS and prepare T and
 // P a chunk ahead, which do not depend on the state.
 // KEEP: instead of o, the corrections E and the states that the backward pass needs.  MAPS:
-// nothing but the state behind a segment, from the state in front of it or, in the
-// workgroups behind those, from the unit matrix with v = 0.
+// nothing but the state behind a segment, from the zero state (segment 0: the first one),
+// and beside it, by as many waves again, from the unit matrix with v = 0.
 enum Mode { READ = 0, KEEP = 1, MAPS = 2 };
 template <typename E, int DK, int W, int MODE> struct ForwardLds {
     using Cf = Cfg<E, DK, W>;
@@ -35,33 +35,27 @@ template <typename E, int DK, int W, int MODE> struct ForwardLds {
     float gb[C];  // of the wave that inverts, of the one that prepares P
 };
 
-// What a workgroup takes: columns `slice` of a head's state (or, unit, of the unit matrix)
+// What a wave takes: columns `slice` of a head's state (or, unit, of the unit matrix)
 // through segment seg of a sequence.
 struct Where {
     int slice, h, b, seg;
-    bool unit;
+    bool unit, idle;
     size_t bh;  // of all heads
     size_t heads;
 };
-template <int MODE> __device__ __forceinline__ Where where(const ForwardArgs& a, unsigned id, unsigned slices, unsigned dk) {
+template <int MODE> __device__ __forceinline__ Where where(const ForwardArgs& a, unsigned id, int cols, int dk, bool unit) {
     Where w{};
+    const unsigned slices = unsigned(MODE == MAPS ? max(a.dv, dk) : a.dv) / unsigned(cols);
     w.heads = size_t(a.B) * a.H;
-    if constexpr (MODE == MAPS) {
-        // segments 0 .. segs - 2 of the values, then 1 .. segs - 2 of the unit matrix
-        const unsigned first = unsigned(w.heads) * slices * unsigned(a.segs - 1);
-        w.unit = id >= first;
-        if (w.unit) {
-            id -= first;
-            slices = slices * dk / unsigned(a.dv);
-        }
-    }
     w.slice = int(id % slices);
     id /= slices;
     w.h = int(id % unsigned(a.H));
     id /= unsigned(a.H);
     w.b = int(id % unsigned(a.B));
-    w.seg = int(id / unsigned(a.B)) + (w.unit ? 1 : 0);
+    w.seg = int(id / unsigned(a.B));
     w.bh = size_t(w.b) * a.H + w.h;
+    w.unit = unit;
+    w.idle = MODE == MAPS && (w.slice * cols >= (unit ? dk : a.dv) || (unit && w.seg == 0));
     return w;
 }
 template <int MODE, int KS>
@@ -69,7 +63,7 @@ __device__ __forceinline__ void state_in(const ForwardArgs& a, const Where& w, f
     const size_t size = size_t(a.dv) * (32 * KS);
     // (segment 0 starts from its own copy: S_T may be S0's buffer)
     const float* S = MODE != MAPS && a.segs > 1 ? a.starts + (w.seg * w.heads) * size : w.seg == 0 ? a.S0 : nullptr;
-    if (w.unit) {
+    if (w.unit || w.idle) {
         unit_state<KS>(st, col, lane);
     } else if (S != nullptr) {
         load_state<KS>(st, S + w.bh * size, col, lane);
@@ -77,13 +71,14 @@ __device__ __forceinline__ void state_in(const ForwardArgs& a, const Where& w, f
 #pragma unroll
         for (int i = 0; i < 2 * KS; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
     }
-    if (MODE == MAPS && w.seg == 0) store_state<KS>(st, a.starts + w.bh * size, col, lane);
+    if (MODE == MAPS && w.seg == 0 && !w.idle) store_state<KS>(st, a.starts + w.bh * size, col, lane);
 }
 template <int MODE, int KS>
 __device__ __forceinline__ void state_out(const ForwardArgs& a, const Where& w, const floatx4 (&st)[2 * KS], int col0, int lane) {
     const size_t size = size_t(a.dv) * (32 * KS);
     const int col = col0 + (lane & 15);
     if constexpr (MODE == MAPS) {
+        if (w.idle) return;
         if (w.unit) store_map<KS>(st, a.maps + ((w.seg - 1) * w.heads + w.bh) * size_t(32 * KS) * (32 * KS), col0, lane);
         else store_state<KS>(st, a.starts + ((w.seg + 1) * w.heads + w.bh) * size, col, lane);
     } else {
@@ -92,33 +87,34 @@ __device__ __forceinline__ void state_out(const ForwardArgs& a, const Where& w, 
 }
 
 template <typename E, int DK, int W, int MODE>
-__global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kernel(ForwardArgs a) {
+__global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W : 0))) void delta_forward_kernel(ForwardArgs a) {
     using Cf = Cfg<E, DK, W>;
     constexpr int NP = Cf::NP, PP = Cf::PP, KT = Cf::KT, KS = Cf::KS, HT = 64 * Cf::NH;
+    constexpr int CW = MODE == MAPS ? 2 * W : W, kThreads = HT + 64 * CW;  // waves of the recurrence
     __shared__ __align__(16) ForwardLds<E, DK, W, MODE> L;
 
-    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), unsigned(a.dv) / Cf::COLS, DK);
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), Cf::COLS, DK, wave >= W);
     const int h = at.h, b = at.b, col0 = at.slice * Cf::COLS;
     Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
     const int start = sq.start, c0 = cut_segment(sq, at.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
-    const int lane = threadIdx.x & 63, wave = wave_id();
 
     const E* q = static_cast<const E*>(a.q) + sq.rq * DK;
     const E* k = static_cast<const E*>(a.k) + sq.rq * DK;
-    const E* v = static_cast<const E*>(a.v) + sq.rv * a.dv + (at.unit ? 0 : col0);
+    const E* v = static_cast<const E*>(a.v) + sq.rv * a.dv + (at.slice * Cf::COLS < a.dv ? col0 : 0);
 
     // zeros: the halves of T and P that no wave writes
-    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += Cf::kThreads)
+    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += kThreads)
         reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
     if constexpr (MODE == READ)
-        for (unsigned i = threadIdx.x; i < 2 * PP * C * C / 8; i += Cf::kThreads)
+        for (unsigned i = threadIdx.x; i < 2 * PP * C * C / 8; i += kThreads)
             reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
     sync_lds();
 
-    if (wave >= W) {
+    if (wave >= CW) {
         // ------------------------------------------------------------------ helpers
-        const int ht = threadIdx.x - 64 * W, hw = wave - W;
+        const int ht = threadIdx.x - 64 * CW, hw = wave - CW;
         Stage<E, DK, HT> sk, sq_;
         Stage<E, Cf::COLS, HT> sv;
         float g = 0.f, be = 0.f;
@@ -207,7 +203,8 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
     }
 
     // --------------------------------------------------------------------- recurrence
-    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
+    const int cw = wave % W;  // the wave's sixteen columns of the slice
+    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * cw + m;
     floatx4 st[KT];
     state_in<MODE, KS>(a, at, st, col, lane);
     const size_t groups =
@@ -215,11 +212,16 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
     sync_lds();
     sync_lds();
     for (int c = 0; c < nc; ++c) {
+        if (MODE == MAPS && at.idle) {
+            sync_lds();
+            sync_lds();
+            continue;
+        }
         const int s = c & 1;
         if constexpr (MODE == KEEP) {
             if (c % a.group == 0)
                 keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK,
-                                  col0 + 16 * wave, lane);
+                                  col0 + 16 * cw, lane);
         }
         // K S (and Q S)
         floatx4 ks[2], qs[2];
@@ -245,12 +247,12 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
             rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
             float vv[4];
             if constexpr (sizeof(E) == 2) {
-                const short4x w = read_tr16(L.v[s] + (t + (m >> 2)) * Cf::LDV + 16 * wave + 4 * (lane & 3));
+                const short4x w = read_tr16(L.v[s] + (t + (m >> 2)) * Cf::LDV + 16 * cw + 4 * (lane & 3));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) vv[e] = bf2f(static_cast<bf16_t>(w[e]));
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) vv[e] = L.v[s][(t + e) * Cf::LDV + 16 * wave + m];
+                for (int e = 0; e < 4; ++e) vv[e] = L.v[s][(t + e) * Cf::LDV + 16 * cw + m];
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[4 * x + e] = (at.unit ? 0.f : vv[e]) - gam[x][e] * ks[x][e];
@@ -305,19 +307,19 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_forward_kerne
         sync_lds();
         sync_lds();
     }
-    state_out<MODE, KS>(a, at, st, col0 + 16 * wave, lane);
+    state_out<MODE, KS>(a, at, st, col0 + 16 * cw, lane);
 }
 
 unsigned workgroups(const ForwardArgs& a, int mode, int dk, int cols) {
-    const unsigned heads = unsigned(a.B) * unsigned(a.H), slices = unsigned(a.dv / cols);
-    if (mode == MAPS) return heads * (slices * unsigned(a.segs - 1) + unsigned(dk / cols) * unsigned(a.segs - 2));
-    return heads * slices * unsigned(std::max(a.segs, 1));
+    const unsigned heads = unsigned(a.B) * unsigned(a.H);
+    if (mode == MAPS) return heads * unsigned(std::max(a.dv, dk) / cols) * unsigned(a.segs - 1);
+    return heads * unsigned(a.dv / cols) * unsigned(std::max(a.segs, 1));
 }
 template <int DK, int W> void forward_dw(const ForwardArgs& a, int mode, hipStream_t st) {
     const unsigned n = workgroups(a, mode, DK, 16 * W);
     constexpr int threads = Cfg<float, DK, W>::kThreads;
     if (mode == KEEP) delta_forward_kernel<float, DK, W, KEEP><<<n, threads, 0, st>>>(a);
-    else if (mode == MAPS) delta_forward_kernel<float, DK, W, MAPS><<<n, threads, 0, st>>>(a);
+    else if (mode == MAPS) delta_forward_kernel<float, DK, W, MAPS><<<n, threads + 64 * W, 0, st>>>(a);
     else delta_forward_kernel<float, DK, W, READ><<<n, threads, 0, st>>>(a);
 }
 template <int DK> void forward_d(const ForwardArgs& a, int mode, hipStream_t st) {
@@ -353,32 +355,33 @@ template <int DK, int DV, int MODE> struct AheadLds {
 };
 
 template <int DK, int DV, int MODE>
-__global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
+__global__ __launch_bounds__(64 * ((MODE == MAPS ? 2 : 1) * AheadLds<DK, DV, MODE>::W + 4)) void delta_ahead_kernel(ForwardArgs a) {
     using Lds = AheadLds<DK, DV, MODE>;
     constexpr int W = Lds::W, COLS = Lds::COLS;
     using Cf = Cfg<bf16_t, DK, W>;
     constexpr int KT = Cf::KT, KS = Cf::KS;
     __shared__ __align__(16) Lds L;
 
-    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), DV / COLS, DK);
+    constexpr int CW = MODE == MAPS ? 2 * W : W, kThreads = 64 * (CW + 4);  // waves of the recurrence
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    const Where at = where<MODE>(a, xcd_order(blockIdx.x, gridDim.x), COLS, DK, wave >= W);
     const int h = at.h, b = at.b, col0 = at.slice * COLS;
     Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
     const int start = sq.start, c0 = cut_segment(sq, at.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
-    const int lane = threadIdx.x & 63, wave = wave_id();
 
-    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += 64 * (W + 4))
+    for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += kThreads)
         reinterpret_cast<u32x4*>(L.t)[i] = u32x4{0, 0, 0, 0};
     if constexpr (MODE == READ)
-        for (unsigned i = threadIdx.x; i < 2 * 2 * C * C / 8; i += 64 * (W + 4))
+        for (unsigned i = threadIdx.x; i < 2 * 2 * C * C / 8; i += kThreads)
             reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
 
-    if (wave >= W) {
-        const int hw = wave - W;
+    if (wave >= CW) {
+        const int hw = wave - CW;
         if (hw == 3) {
             const bf16_t* q = static_cast<const bf16_t*>(a.q) + sq.rq * DK;
             const bf16_t* k = static_cast<const bf16_t*>(a.k) + sq.rq * DK;
-            const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + (at.unit ? 0 : col0);
+            const bf16_t* v = static_cast<const bf16_t*>(a.v) + sq.rv * DV + (at.slice * COLS < DV ? col0 : 0);
             const uint32_t lk = lds_address(L.k), lq = lds_address(L.q), lv = lds_address(L.v);
             float g = 0.f, be = 0.f;
             auto gates = [&](int c) {
@@ -445,12 +448,13 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ah
     }
 
     // --------------------------------------------------------------------- recurrence
-    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
+    const int cw = wave % W;  // the wave's sixteen columns of the slice
+    const int g = lane >> 4, m = lane & 15, col = col0 + 16 * cw + m;
     floatx4 st[KT];
     state_in<MODE, KS>(a, at, st, col, lane);
     const size_t groups =
         MODE == KEEP ? group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group : 0;
-    bf16_t* out = static_cast<bf16_t*>(MODE == KEEP ? a.keep_E : a.o) + sq.rv * DV + col0 + 16 * wave + 4 * g;
+    bf16_t* out = static_cast<bf16_t*>(MODE == KEEP ? a.keep_E : a.o) + sq.rv * DV + col0 + 16 * cw + 4 * g;
     sync_lds();
     sync_lds();
     sync_lds();
@@ -483,12 +487,16 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ah
     };
     if (nc > 0) fetch(0);
     for (int c = 0; c < nc; ++c) {
+        if (MODE == MAPS && at.idle) {
+            sync_lds();
+            continue;
+        }
         const int s = c & 3;
         if constexpr (MODE == KEEP) {
             if (c % a.group == 0)
                 keep_state<bf16_t, KS>(
                     st, static_cast<bf16_t*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK,
-                    col0 + 16 * wave, lane);
+                    col0 + 16 * cw, lane);
         }
         floatx4 gam[2], be[2], rest[2];
         short4x vw[2];
@@ -500,7 +508,7 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ah
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
             gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
-            vw[x] = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * wave + ((lane & 3) >> 1)) + 4 * (lane & 1));
+            vw[x] = read_tr16(L.v[s] + value_at<COLS>(t + (m >> 2), 2 * cw + ((lane & 3) >> 1)) + 4 * (lane & 1));
             ks[x] = qs[x] = floatx4{0.f, 0.f, 0.f, 0.f};
         }
         const float last = L.gam[s][C - 1];
@@ -596,14 +604,14 @@ __global__ __launch_bounds__(64 * (AheadLds<DK, DV, MODE>::W + 4)) void delta_ah
         sync_lds();
     }
     if (MODE != MAPS && nc > 0) results(nc - 1, sq.len - (nc - 1) * C);
-    state_out<MODE, KS>(a, at, st, col0 + 16 * wave, lane);
+    state_out<MODE, KS>(a, at, st, col0 + 16 * cw, lane);
 }
 
 template <int DK, int DV> void ahead_go(const ForwardArgs& a, int mode, hipStream_t st) {
     constexpr int W = AheadLds<DK, DV, READ>::W, threads = 64 * (W + 4);
     const unsigned n = workgroups(a, mode, DK, 16 * W);
     if (mode == KEEP) delta_ahead_kernel<DK, DV, KEEP><<<n, threads, 0, st>>>(a);
-    else if (mode == MAPS) delta_ahead_kernel<DK, DV, MAPS><<<n, threads, 0, st>>>(a);
+    else if (mode == MAPS) delta_ahead_kernel<DK, DV, MAPS><<<n, threads + 64 * W, 0, st>>>(a);
     else delta_ahead_kernel<DK, DV, READ><<<n, threads, 0, st>>>(a);
 }
 template <int DK> void ahead_dv(const ForwardArgs& a, int mode, hipStream_t st) {
@@ -619,36 +627,68 @@ void forward_bf16(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
 
 // ------------------------------------------------------------------- segments' states
 // starts[g + 1] <- M_g starts[g] + starts[g + 1] for g = 1 .. segs - 2 (starts[1] is there
-// already), 16 columns of a head's states per wave, in the order of the recurrence.  A step
-// takes about 4 us at d_k 128: a map's 64 KB on their way from memory, and their products.
+// already), in the order of the recurrence.  A workgroup takes 16 columns of a head's
+// states, a wave 32 rows of them; the state's planes meet in LDS, the next map is on its
+// way during a step.
 template <int DK>
-__global__ __launch_bounds__(256) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* starts) {
+__global__ __launch_bounds__(2 * DK) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* starts) {
     constexpr int KS = DK / 32;
-    const int lane = threadIdx.x & 63, wave = wave_id();
-    const int groups = (dv + 63) / 64;
-    const size_t bh = blockIdx.x / groups, size = size_t(dv) * DK;
-    const int col = (blockIdx.x % groups) * 64 + 16 * wave + (lane & 15);
-    if (col >= dv) return;
-    floatx4 st[2 * KS];
-    load_state<KS>(st, starts + (size_t(heads) + bh) * size, col, lane);
+    __shared__ __align__(16) bf16x8 planes[2][KS][3][64];
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
+    const size_t bh = blockIdx.x / unsigned(dv / 16), size = size_t(dv) * DK;
+    const int col = int(blockIdx.x % unsigned(dv / 16)) * 16 + (lane & 15);
+    const size_t mine = bh * size + size_t(col) * DK + 32 * wave + 8 * g;  // this lane's eight values of a state
+    floatx4 st[2], next[2], m[2][KS][2];
+    auto state = [&](int s, floatx4 (&x)[2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = *reinterpret_cast<const floatx4*>(starts + size_t(s) * heads * size + mine + 4 * h);
+    };
+    auto map = [&](int s) {
+        const float* M = maps + ((s - 1) * size_t(heads) + bh) * size_t(DK) * DK + 8 * g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    m[h][j][v] = *reinterpret_cast<const floatx4*>(M + (32 * wave + paired_row(lane, h)) * DK + 32 * j + 4 * v);
+    };
+    state(1, st);
+    if (segs > 2) {
+        map(1);
+        state(2, next);
+    }
     for (int s = 1; s < segs - 1; ++s) {
-        const float* M = maps + ((s - 1) * size_t(heads) + bh) * size_t(DK) * DK + 8 * (lane >> 4);
-        float* S = starts + ((s + 1) * size_t(heads) + bh) * size;
-        Planes<3> sp[KS];
+        const Planes<3> p = state_planes<2>(st, 0);
 #pragma unroll
-        for (int j = 0; j < KS; ++j) sp[j] = state_planes<2 * KS>(st, j);
-        load_state<KS>(st, S, col, lane);
+        for (int n = 0; n < 3; ++n) planes[s & 1][wave][n][lane] = p.p[n];
+        Planes<3> mp[2][KS];
 #pragma unroll
-        for (int i = 0; i < 2 * KS; ++i) {
-            const float* row = M + (32 * (i >> 1) + paired_row(lane, i & 1)) * DK;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
                 float f[8];
-                load_vec<float, 8>(row + 32 * j, f);
-                st[i] = product<2>(split8<3>(f), sp[j], st[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = m[h][j][e / 4][e % 4];
+                mp[h][j] = split8<3>(f);
             }
+        st[0] = next[0];
+        st[1] = next[1];
+        if (s + 1 < segs - 1) {
+            map(s + 1);
+            state(s + 2, next);
         }
-        store_state<KS>(st, S, col, lane);
+        sync_lds();
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+            Planes<3> q;
+#pragma unroll
+            for (int n = 0; n < 3; ++n) q.p[n] = planes[s & 1][j][n][lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) st[h] = product<2>(mp[h][j], q, st[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<floatx4*>(starts + size_t(s + 1) * heads * size + mine + 4 * h) = st[h];
     }
 }
 
@@ -767,22 +807,22 @@ hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hi
 }
 
 // The count is chosen by an estimate of the launches' rounds of 256 workgroups: a chunk of
-// 32 tokens takes 1.7 us with the read-out and 1.4 without (d 128, bfloat16), a step of the
-// composition 4 us, two more launches 8.
+// 32 tokens takes 1.9 us with the read-out and 2.3 in the maps (d 128, bfloat16), a step of
+// the composition 1.5 us, two more launches 8.
 Segments segments_of(const kdn_delta_desc* d, bool packed, int group) {
     Segments s{};
     s.count = 1;
     s.total = 16;
     const int64_t heads = int64_t(d->B) * d->H, cols = d->d_v == 32 || d->d_k == 32 ? 32 : 64;
     const int64_t tokens = packed ? d->T / std::max(d->B, 1) : d->T, nc = (tokens + C - 1) / C;
-    const int64_t w = heads * (d->d_v / cols), wk = heads * (d->d_k / cols);
+    const int64_t w = heads * (d->d_v / cols), wm = heads * (std::max(d->d_v, d->d_k) / cols);
     if (heads == 0 || w > 128 || nc < 16) return s;
     auto rounds = [](int64_t n) { return double((n + 255) / 256); };
     const double scale = 0.5 + d->d_k / 256.0;
-    double best = 0.8 * scale * 1.7 * nc * rounds(w);
+    double best = 0.8 * scale * 1.9 * nc * rounds(w);
     for (int n = 2; n <= 64 && n * 4 <= nc; ++n) {
         const int64_t per = ((nc + n - 1) / n + group - 1) / group * group;
-        const double t = scale * per * (1.4 * rounds(w * (n - 1) + wk * (n - 2)) + 1.7 * rounds(w * n)) + 4.0 * (n - 2) + 8.0;
+        const double t = scale * per * (2.3 * rounds(wm * (n - 1)) + 1.9 * rounds(w * n)) + 1.5 * (n - 2) + 8.0;
         if (t < best) {
             best = t;
             s.count = n;
@@ -807,9 +847,9 @@ hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtyp
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.count == 2) return e;
     const int heads = a.B * a.H;
-    const unsigned n = unsigned(heads) * unsigned((a.dv + 63) / 64);
-    if (dk == 32) delta_compose_kernel<32><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
-    else if (dk == 64) delta_compose_kernel<64><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
+    const unsigned n = unsigned(heads) * unsigned(a.dv / 16);
+    if (dk == 32) delta_compose_kernel<32><<<n, 64, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
+    else if (dk == 64) delta_compose_kernel<64><<<n, 128, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
     else delta_compose_kernel<128><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
     return hipGetLastError();
 }
