@@ -113,8 +113,8 @@ class KdnDeltaDesc(ctypes.Structure):
 class KdnRotaryDesc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "T", "H", "Hk", "d", "rot", "dtype",
                                                "interleaved")] + [("eps", ctypes.c_float)] +
-                [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "dq_stride",
-                                                   "dk_stride")])
+                [(f"{n}_stride_{of}", ctypes.c_int64) for n in ("q", "k", "dq", "dk")
+                 for of in ("batch", "token", "head")])
 
 
 class KdnError(RuntimeError):
@@ -1137,41 +1137,41 @@ def gated_delta_step(q, k, v, g, beta, S, slot=None, scale=None, out=None):
     return o
 
 
-def _rows_view(name, x, dev):
-    """A view of token rows [B,T,H,d]: on `dev`, columns contiguous."""
+def _row_strides(name, x, at):
+    """Batch, token and head strides of a view of token rows [B,T,H,d] on GPU `at`, columns
+    contiguous (0 for those of single entries, which no address depends on)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not x.is_cuda:
         raise KdnError(f"{name} must be on a GPU (no CPU path exists)")
-    if x.dim() != 4 or (x.stride(3) != 1 and x.shape[3] > 1):
+    if x.get_device() != at:
+        raise ValueError(f"{name} is on {x.device}, the other tensors are on cuda:{at}")
+    if x.dim() != 4:
         raise ValueError(f"{name} must be [B,T,H,d] with contiguous columns")
-    if dev is not None and x.device != dev:
-        raise ValueError(f"{name} is on {x.device}, the other tensors are on {dev}")
-    return x.device
+    B, T, H, d = x.shape
+    b, t, h, c = x.stride()
+    if c != 1 and d > 1:
+        raise ValueError(f"{name} must be [B,T,H,d] with contiguous columns")
+    return (b if B > 1 else 0, t if T > 1 else 0, h if H > 1 else 0)
 
 
-def _row_strides(x):
-    """Batch, token and head strides of a view of token rows; those of single entries, which
-    no address depends on, as 0."""
-    s = x.stride()
-    return (ctypes.c_int64 * 3)(*(s[i] if x.shape[i] > 1 else 0 for i in range(3)))
-
-
-def _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved):
-    if k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
-        raise ValueError("q and k must agree in all but their heads, and in dtype")
+def _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved, at, out=()):
+    strides = (*_row_strides("q", q, at), *_row_strides("k", k, at))
     B, T, H, d = q.shape
+    kB, kT, Hk, kd = k.shape
+    if k.dtype != q.dtype or kB != B or kT != T or kd != d:
+        raise ValueError("q and k must agree in all but their heads, and in dtype")
     _shaped("q_weight", q_weight, torch.float32, (d,))
     _shaped("k_weight", k_weight, torch.float32, (d,))
     if (position is None) != (inv_freq is None):
         raise ValueError("position and inv_freq go together")
-    _shaped("position", position, torch.int32, (B, T))
     rot = 0
-    if inv_freq is not None:
+    if position is not None:
+        _shaped("position", position, torch.int32, (B, T))
         rot = 2 * inv_freq.numel()
         _shaped("inv_freq", inv_freq, torch.float32, (rot // 2,))
-    return KdnRotaryDesc(*_int32(B, T, H, k.shape[2], d, rot), _dtype_code(q.dtype),
-                         int(interleaved), eps, _row_strides(q), _row_strides(k))
+    return KdnRotaryDesc(*_int32(B, T, H, Hk, d, rot), _dtype_code(q.dtype), int(interleaved), eps,
+                         *strides, *out)
 
 
 def qk_norm_rotary(q, k, q_weight, k_weight, position, inv_freq, eps=1e-6, interleaved=False):
@@ -1185,14 +1185,14 @@ def qk_norm_rotary(q, k, q_weight, k_weight, position, inv_freq, eps=1e-6, inter
     roots q_rstd [B,H,T], k_rstd [B,Hk,T] float32)."""
     dev = _tensors(("q_weight", q_weight), ("k_weight", k_weight), ("position", position),
                    ("inv_freq", inv_freq))
-    dev = _rows_view("k", k, _rows_view("q", q, dev))
-    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved)
-    out = [_empty((n.B, h, n.T, n.d), q.dtype, dev) for h in (n.H, n.Hk)]
-    rstd = [_empty((n.B, h, n.T), torch.float32, dev) for h in (n.H, n.Hk)]
+    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, eps, interleaved, dev.index)
+    B, T, H, Hk, d, t = n.B, n.T, n.H, n.Hk, n.d, q.dtype
+    qo, ko = _empty((B, H, T, d), t, dev), _empty((B, Hk, T, d), t, dev)
+    qr, kr = _empty((B, H, T), torch.float32, dev), _empty((B, Hk, T), torch.float32, dev)
     _launch("kdn_qk_norm_rotary", dev, ctypes.byref(n), q.data_ptr(), k.data_ptr(),
             q_weight.data_ptr(), k_weight.data_ptr(), _ptr(position), _ptr(inv_freq),
-            out[0].data_ptr(), out[1].data_ptr(), rstd[0].data_ptr(), rstd[1].data_ptr())
-    return (*out, *rstd)
+            qo.data_ptr(), ko.data_ptr(), qr.data_ptr(), kr.data_ptr())
+    return qo, ko, qr, kr
 
 
 def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, position, inv_freq, q_rstd,
@@ -1205,19 +1205,18 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, position, 
     dev = _tensors(("dq_out", dq_out), ("dk_out", dk_out), ("q_weight", q_weight),
                    ("k_weight", k_weight), ("position", position), ("inv_freq", inv_freq),
                    ("q_rstd", q_rstd), ("k_rstd", k_rstd))
-    _rows_view("k", k, _rows_view("q", q, dev))
-    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, 0.0, interleaved)
-    for name, x, r, h in (("dq_out", dq_out, q_rstd, n.H), ("dk_out", dk_out, k_rstd, n.Hk)):
-        _shaped(name, x, q.dtype, (n.B, h, n.T, n.d))
-        _shaped(name[1] + "_rstd", r, torch.float32, (n.B, h, n.T))
     if out is None:
-        dq, dk = (_empty(tuple(x.shape), q.dtype, dev) for x in (q, k))
+        dq, dk = _empty(tuple(q.shape), q.dtype, dev), _empty(tuple(k.shape), q.dtype, dev)
     else:
         dq, dk = out
-        for name, x, like in (("dq", dq, q), ("dk", dk, k)):
-            _rows_view(name, x, dev)
-            _shaped(name, x, q.dtype, like.shape)
-    n.dq_stride, n.dk_stride = _row_strides(dq), _row_strides(dk)
+        _shaped("dq", dq, q.dtype, q.shape)
+        _shaped("dk", dk, q.dtype, k.shape)
+    at = dev.index
+    n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, 0.0, interleaved, at,
+                     (*_row_strides("dq", dq, at), *_row_strides("dk", dk, at)))
+    for name, x, r, h in (("q", dq_out, q_rstd, n.H), ("k", dk_out, k_rstd, n.Hk)):
+        _shaped(f"d{name}_out", x, q.dtype, (n.B, h, n.T, n.d))
+        _shaped(f"{name}_rstd", r, torch.float32, (n.B, h, n.T))
     dw = _empty((2, n.d), torch.float32, dev)
     need = load_library().kdn_qk_norm_rotary_backward_workspace_bytes(ctypes.byref(n))
     ws = _empty((max(need, 16),), torch.uint8, dev)

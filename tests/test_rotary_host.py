@@ -20,9 +20,8 @@ def lib():
 
 
 def _desc(B=2, T=10, H=4, Hk=2, d=64, rot=32, dtype=kdn.BF16, interleaved=0, eps=1e-6, strides=None):
-    three = ctypes.c_int64 * 3
     s = strides or (H * d * T, H * d, d)
-    return kdn.KdnRotaryDesc(B, T, H, Hk, d, rot, dtype, interleaved, eps, three(*s), three(*s), three(*s), three(*s))
+    return kdn.KdnRotaryDesc(B, T, H, Hk, d, rot, dtype, interleaved, eps, *s, *s, *s, *s)
 
 
 BAD = [
