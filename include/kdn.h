@@ -595,8 +595,10 @@ kdn_status kdn_gated_scan_step(const kdn_scan_desc *s, const void *x, const void
  * an infinity or NaN in a token makes outputs of its own block and of later tokens
  * of its head non-finite (a value's: its column alone), and nothing of other
  * sequences and heads.
- * Sums and states have float32's accuracy for both types (kernels: products of
- * operands split into bfloat16 parts that together hold all of a float32's bits). */
+ * States and sums are float32; float32 inputs keep float32's accuracy throughout (products
+ * of operands split into bfloat16 parts that together hold all of its bits).  With bfloat16
+ * inputs a state takes part in the products with k by 18 of its bits, and in o, which is
+ * rounded to bfloat16, by 16. */
 typedef struct {
     int32_t B, H, Hk, T, d_k, d_v;
     int32_t dtype;      /* kdn_dtype */

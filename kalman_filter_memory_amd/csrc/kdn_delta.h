@@ -13,7 +13,10 @@
 // ones' rate), with every float32 operand written as the sum of three bfloat16 planes
 // (8 bits of the mantissa each: nothing is lost) and the partial products below 2^-24
 // left out, so states, corrections and gradients of the state carry float32's accuracy.
-// bfloat16 inputs are one plane, exactly.
+// bfloat16 inputs are one plane, exactly.  Beside them the state enters K S in two planes:
+// it is off by at most 2^-18 of its elements there (measured: 2 to 5 10^-7 of S_T in the
+// 2-norm, 1.5 10^-7 with three planes, for 5 % of the time; two planes of U, which go into
+// the state itself, would leave 2.6 10^-6 and save nothing).
 #pragma once
 
 #include "../../include/kdn.h"

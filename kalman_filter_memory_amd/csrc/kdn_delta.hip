@@ -530,21 +530,13 @@ __global__ __launch_bounds__(64 * ((MODE == MAPS ? 2 : 1) * AheadLds<DK, DV, MOD
         for (int j = 0; j < KS; ++j) {
             sp[j].p[1] = pack8(r1[2 * j], r1[2 * j + 1]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j].p[0], ks[x]);
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j].p[1], r1[2 * j + x]);
+                for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j].p[n], ks[x]);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[2 * j + x][e] *= last;
-        }
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-            const bf16x8 p2 = pack8(r1[2 * j], r1[2 * j + 1]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j].p[1], ks[x]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) ks[x] = Mma<bf16_t>::mma(kf[x][j].p[0], p2, ks[x]);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) tf[x] = square_frag<3>(L.t[c & 1], x, lane);

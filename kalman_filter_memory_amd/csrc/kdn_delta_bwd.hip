@@ -454,19 +454,11 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
         for (int j = 0; j < KS; ++j) {
             sp[j] = pack8(r1[2 * j], r1[2 * j + 1]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) r1[2 * j + x] = Mma<bf16_t>::mma(minus[x], sp[j], r1[2 * j + x]);
-#pragma unroll
             for (int x = 0; x < 2; ++x) kd[x] = Mma<bf16_t>::mma(kf[x][j].p[0], sp[j], kd[x]);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) st[2 * j + x][e] *= last;
-        }
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-            const bf16x8 p2 = pack8(r1[2 * j], r1[2 * j + 1]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) kd[x] = Mma<bf16_t>::mma(kf[x][j].p[0], p2, kd[x]);
         }
         // D <- gamma_C D + Q^T (scale gamma dO), beside the way to X
         {
