@@ -356,6 +356,10 @@ template <typename E, int DK_, int W_> struct Cfg {
     static constexpr int PP = sizeof(E) == 2 ? 2 : 3;  // planes behind the read-out, which is rounded to E
     static constexpr int DK = DK_, W = W_, KT = DK / 16, KS = DK / 32;
     static constexpr int NH = 4;  // helper waves
+    // float32: whether the planes of four chunks' keys fit LDS, so that the system of the
+    // chunk after the next can be formed beside the inversion of the next one's
+    static constexpr bool kAhead = DK <= 64;
+    static constexpr int KSLOTS = kAhead ? 4 : 2, QSLOTS = kAhead ? 3 : 2, GSLOTS = kAhead ? 4 : 2;
     static constexpr int kThreads = 64 * (W + NH);
     static constexpr int COLS = 16 * W;
     static constexpr int LDV = COLS + (sizeof(E) == 2 ? 8 : 4);
@@ -417,7 +421,7 @@ template <typename E, int D, int THREADS, int ROWS = C> struct Stage {
             r[i] = load_raw8<E>(x + size_t(row) * stride + 8 * p, e < kAll && row < rows);
         }
     }
-    template <typename F> __device__ __forceinline__ void each(int h, F f) {
+    template <typename F> __device__ __forceinline__ void each(int h, F f) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = h + THREADS * i;

@@ -23,16 +23,15 @@ namespace {
 enum Mode { READ = 0, KEEP = 1, MAPS = 2 };
 template <typename E, int DK, int W, int MODE> struct ForwardLds {
     using Cf = Cfg<E, DK, W>;
-    bf16_t k[2][Cf::NP * C * DK];
-    bf16_t q[MODE ? 1 : 2][MODE ? 8 : Cf::NP * C * DK];
+    bf16_t k[Cf::KSLOTS][Cf::NP * C * DK];
+    bf16_t q[MODE ? 1 : Cf::QSLOTS][MODE ? 8 : Cf::NP * C * DK];
     E v[2][C * Cf::LDV];
     bf16_t t[2][3 * C * C];
     bf16_t p[MODE ? 1 : 2][MODE ? 8 : Cf::PP * C * C];
-    float a[C * kLdA];
-    float tmp[32 * kLdT];
-    float gam[2][C], rest[2][C], beta[2][C];
-    LogSum G[2][C];
-    float gb[C];  // of the wave that inverts, of the one that prepares P
+    float a[Cf::kAhead ? 2 : 1][C * kLdA];
+    float tmp[Cf::kAhead ? 2 : 1][32 * kLdT];
+    float gam[Cf::GSLOTS][C], rest[Cf::GSLOTS][C], beta[Cf::GSLOTS][C];
+    LogSum G[Cf::GSLOTS][C];
 };
 
 // What a wave takes: columns `slice` of a head's state (or, unit, of the unit matrix)
@@ -116,88 +115,132 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
         // ------------------------------------------------------------------ helpers
         const int ht = threadIdx.x - 64 * CW, hw = wave - CW;
         Stage<E, DK, HT> sk, sq_;
-        Stage<E, Cf::COLS, HT> sv;
+        Stage<E, Cf::COLS, HT> s3;
         float g = 0.f, be = 0.f;
-        auto load = [&](int c) {
-            const int t0 = c * C, rows = sq.len - t0;
-            sk.load(k + size_t(t0) * DK, DK, rows, ht);
-            if constexpr (MODE == READ) sq_.load(q + size_t(t0) * DK, DK, rows, ht);
-            sv.load(v + size_t(t0) * a.dv, a.dv, rows, ht);
-        };
-        auto gates = [&](int c) {  // of chunk c, token lane % 32
-            const int t = c * C + (lane & 31);
+        // (chunks in the order of the recurrence: the c-th begins at this token)
+        auto token = [&](int c) { return c * C; };
+        auto load_k = [&](int c) { sk.load(k + size_t(token(c)) * DK, DK, sq.len - token(c), ht); };
+        auto load_q = [&](int c) { if constexpr (MODE == READ) sq_.load(q + size_t(token(c)) * DK, DK, sq.len - token(c), ht); };
+        auto load_3 = [&](int c) { s3.load(v + size_t(token(c)) * a.dv, a.dv, sq.len - token(c), ht); };
+        auto gates = [&](int c) {
+            const int t = token(c) + (lane & 31);
             g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
             be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
         };
-        auto put = [&](int c) {
-            const int s = c & 1;
-            sk.each(ht, [&](const Raw8<E>& r, int row, int p) {
-                const auto x = planes_of<E>(r);
+        auto put_rows = [&](const Stage<E, DK, HT>& st, bf16_t* x) {
+            st.each(ht, [&](const Raw8<E>& r, int row, int p) {
+                const auto y = planes_of<E>(r);
 #pragma unroll
                 for (int n = 0; n < NP; ++n)
-                    *reinterpret_cast<bf16x8*>(L.k[s] + n * C * DK + Cf::Tile::at(row, p)) = x.p[n];
+                    *reinterpret_cast<bf16x8*>(x + n * C * DK + Cf::Tile::at(row, p)) = y.p[n];
             });
-            if constexpr (MODE == READ)
-                sq_.each(ht, [&](const Raw8<E>& r, int row, int p) {
-                    const auto x = planes_of<E>(r);
-#pragma unroll
-                    for (int n = 0; n < NP; ++n)
-                        *reinterpret_cast<bf16x8*>(L.q[s] + n * C * DK + Cf::Tile::at(row, p)) = x.p[n];
-                });
-            sv.each(ht, [&](const Raw8<E>& r, int row, int p) {
+        };
+        auto put_k = [&](int c) { put_rows(sk, L.k[c % Cf::KSLOTS]); };
+        auto put_q = [&](int c) { if constexpr (MODE == READ) put_rows(sq_, L.q[c % Cf::QSLOTS]); };
+        auto put_3 = [&](int c) {
+            s3.each(ht, [&](const Raw8<E>& r, int row, int p) {
 #pragma unroll
                 for (int i = 0; i < Raw8<E>::N; ++i)
-                    reinterpret_cast<u32x4*>(L.v[s] + row * Cf::LDV + 8 * p)[i] = r.w[i];
+                    reinterpret_cast<u32x4*>(L.v[c & 1] + row * Cf::LDV + 8 * p)[i] = r.w[i];
             });
         };
-        auto prepare = [&](int c) {  // T, or P and the gates, of chunk c
-            const int s = c & 1;
+        auto sums = [&](int c) {
+            const int s = c % Cf::GSLOTS;
             const LogSum G = log_sums<C>(g, lane);
-            if (hw == 0) {
-                if (lane < C) {
-                    L.G[0][lane] = G;
-                    L.gb[lane] = be;
-                }
-                wave_lds_fence();
-                system_of<Cf, false>(L.k[s], L.G[0], L.gb, L.a, lane);
-                wave_lds_fence();
-                invert<false>(L.a, L.tmp, L.t[s], lane);
-            } else if (hw == 1) {
-                const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
-                if (lane < C) {
-                    L.G[1][lane] = G;
-                    L.gam[s][lane] = decay_of(G);
-                    L.rest[s][lane] = decay_between(last, G);
-                    L.beta[s][lane] = be;
-                }
-                if constexpr (MODE == READ) {
-                    wave_lds_fence();
-                    readout_of<Cf, false, PP>(L.q[s], L.k[s], L.G[1], a.scale, C, L.p[s], lane);
-                }
+            const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
+            if (lane < C) {
+                L.G[s][lane] = G;
+                L.gam[s][lane] = decay_of(G);
+                L.rest[s][lane] = decay_between(last, G);
+                L.beta[s][lane] = be;
             }
         };
-        if (nc > 0) {
-            load(0);
-            gates(0);
-            put(0);
-            if (nc > 1) load(1);
-        }
-        sync_lds();
-        if (nc > 0) prepare(0);
-        if (nc > 1) {
-            gates(1);
-            put(1);
-        }
-        sync_lds();
-        for (int c = 0; c < nc; ++c) {
-            if (c + 2 < nc) load(c + 2);
-            if (c + 1 < nc) {
-                prepare(c + 1);
-                if (c + 2 < nc) gates(c + 2);
+        auto system = [&](int c, int w) {
+            system_of<Cf, false>(L.k[c % Cf::KSLOTS], L.G[c % Cf::GSLOTS], L.beta[c % Cf::GSLOTS], L.a[w], lane);
+        };
+        auto inverse = [&](int c, int w) { invert<false>(L.a[w], L.tmp[w], L.t[c & 1], lane); };
+        auto readout = [&](int c) {
+            if constexpr (MODE == READ)
+                readout_of<Cf, false, PP>(L.q[c % Cf::QSLOTS], L.k[c % Cf::KSLOTS], L.G[c % Cf::GSLOTS], a.scale, C, L.p[c & 1], lane);
+        };
+        if constexpr (Cf::kAhead) {
+            // Interval c: rows of k go to LDS three chunks ahead, of q two, the third tensor's
+            // one; the waves take turns with a chunk's system and its inversion.
+            if (nc > 0) {
+                load_k(0);
+                gates(0);
+                put_k(0);
+                if (hw == 3) sums(0);
+                load_q(0);
+                load_3(0);
             }
-            sync_lds();  // chunk c is done with
-            if (c + 2 < nc) put(c + 2);
+            if (nc > 1) {
+                load_k(1);
+                gates(1);
+            }
             sync_lds();
+            for (int c = -2; c < nc; ++c) {
+                if (c + 3 < nc) {
+                    put_k(c + 3);
+                    if (hw == 3) sums(c + 3);
+                    if (c + 4 < nc) {
+                        load_k(c + 4);
+                        gates(c + 4);
+                    }
+                }
+                if (c + 2 < nc) {
+                    put_q(c + 2);
+                    if (c + 3 < nc) load_q(c + 3);
+                }
+                if (c >= -1 && c + 1 < nc) {
+                    put_3(c + 1);
+                    if (c + 2 < nc) load_3(c + 2);
+                }
+                if (hw == 2) {
+                    if (c >= -1 && c + 1 < nc) readout(c + 1);
+                } else if (hw < 2) {
+                    if ((c & 1) == hw) {
+                        if (c + 2 < nc) system(c + 2, hw);
+                    } else if (c >= -1 && c + 1 < nc) {
+                        inverse(c + 1, hw);
+                    }
+                }
+                sync_lds();
+            }
+        } else {
+            auto load = [&](int c) {
+                load_k(c);
+                load_q(c);
+                load_3(c);
+                gates(c);
+            };
+            auto put = [&](int c) {
+                put_k(c);
+                put_q(c);
+                put_3(c);
+                if (hw == 3) sums(c);
+            };
+            if (nc > 0) {
+                load(0);
+                put(0);
+                if (nc > 1) load(1);
+            }
+            sync_lds();
+            for (int c = -1; c < nc; ++c) {
+                if (c >= 0 && c + 2 < nc) load(c + 2);
+                if (c + 1 < nc) {
+                    if (hw == 0) {
+                        system(c + 1, 0);
+                        wave_lds_fence();
+                        inverse(c + 1, 0);
+                    } else if (hw == 1) {
+                        readout(c + 1);
+                    }
+                }
+                sync_lds();  // chunk c is done with
+                if (c + 2 < nc) put(c + 2);
+                sync_lds();
+            }
         }
         return;
     }
@@ -211,13 +254,14 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
         MODE == KEEP ? group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group : 0;
     sync_lds();
     sync_lds();
+    sync_lds();
     for (int c = 0; c < nc; ++c) {
         if (MODE == MAPS && at.idle) {
             sync_lds();
-            sync_lds();
+            if constexpr (!Cf::kAhead) sync_lds();
             continue;
         }
-        const int s = c & 1;
+        const int ks_ = c % Cf::KSLOTS, sg = c % Cf::GSLOTS;
         if constexpr (MODE == KEEP) {
             if (c % a.group == 0)
                 keep_state<E, KS>(st, static_cast<E*>(a.keep_S) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK,
@@ -231,10 +275,10 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
         for (int j = 0; j < KS; ++j) {
             const Planes<3> sp = state_planes<KT>(st, j);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) ks[x] = product<2>(row_frag<Cf>(L.k[s], x, j, lane), sp, ks[x]);
+            for (int x = 0; x < 2; ++x) ks[x] = product<2>(row_frag<Cf>(L.k[ks_], x, j, lane), sp, ks[x]);
             if constexpr (MODE == READ)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) qs[x] = product<PP - 1>(row_frag<Cf>(L.q[s], x, j, lane), sp, qs[x]);
+                for (int x = 0; x < 2; ++x) qs[x] = product<PP - 1>(row_frag<Cf>(L.q[c % Cf::QSLOTS], x, j, lane), sp, qs[x]);
         }
         // E = T (V - gamma K S); this lane's tokens are 8 g + 0..7 of the chunk
         floatx4 gam[2], be[2], rest[2];
@@ -242,17 +286,17 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
-            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
-            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[s][t]);
-            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
+            gam[x] = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
+            be[x] = *reinterpret_cast<const floatx4*>(&L.beta[sg][t]);
+            rest[x] = *reinterpret_cast<const floatx4*>(&L.rest[sg][t]);
             float vv[4];
             if constexpr (sizeof(E) == 2) {
-                const short4x w = read_tr16(L.v[s] + (t + (m >> 2)) * Cf::LDV + 16 * cw + 4 * (lane & 3));
+                const short4x w = read_tr16(L.v[c & 1] + (t + (m >> 2)) * Cf::LDV + 16 * cw + 4 * (lane & 3));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) vv[e] = bf2f(static_cast<bf16_t>(w[e]));
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) vv[e] = L.v[s][(t + e) * Cf::LDV + 16 * cw + m];
+                for (int e = 0; e < 4; ++e) vv[e] = L.v[c & 1][(t + e) * Cf::LDV + 16 * cw + m];
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[4 * x + e] = (at.unit ? 0.f : vv[e]) - gam[x][e] * ks[x][e];
@@ -261,7 +305,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
         floatx4 ee[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-            ee[x] = product<2>(square_frag<3>(L.t[s], x, lane), rp, floatx4{0.f, 0.f, 0.f, 0.f});
+            ee[x] = product<2>(square_frag<3>(L.t[c & 1], x, lane), rp, floatx4{0.f, 0.f, 0.f, 0.f});
         float u[8], ub[8];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -272,11 +316,11 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
             }
         // S <- gamma_C S + K^T (rest U)
         const Planes<3> up = split8<3>(ub);
-        const float last = L.gam[s][C - 1];
+        const float last = L.gam[sg][C - 1];
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
             const floatx4 w = {last * st[i][0], last * st[i][1], last * st[i][2], last * st[i][3]};
-            st[i] = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), up, w);
+            st[i] = product<2>(col_frag<Cf>(L.k[ks_], i / 2, i % 2, lane), up, w);
         }
         const int rows = sq.len - c * C;
         if constexpr (MODE == KEEP) {
@@ -296,7 +340,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
                 floatx4 o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = a.scale * gam[x][e] * qs[x][e];
-                o = product<PP - 1>(square_frag<PP>(L.p[s], x, lane), uo, o);
+                o = product<PP - 1>(square_frag<PP>(L.p[c & 1], x, lane), uo, o);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = 8 * g + 4 * x + e;
@@ -305,7 +349,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads + (MODE == MAPS ? 64 * W :
             }
         }
         sync_lds();
-        sync_lds();
+        if constexpr (!Cf::kAhead) sync_lds();
     }
     state_out<MODE, KS>(a, at, st, col0 + 16 * cw, lane);
 }

@@ -42,14 +42,13 @@ struct BackwardArgs {
 // ------------------------------------------------------------------ backward recurrence
 template <typename E, int DK, int W> struct ReverseLds {
     using Cf = Cfg<E, DK, W>;
-    bf16_t k[2][Cf::NP * C * DK], q[2][Cf::NP * C * DK];
+    bf16_t k[Cf::KSLOTS][Cf::NP * C * DK], q[Cf::QSLOTS][Cf::NP * C * DK];
     bf16_t d[2][Cf::NP * C * Cf::LDO];
     bf16_t t[2][3 * C * C], p[2][3 * C * C];
-    float a[C * kLdA];
-    float tmp[32 * kLdT];
-    float gam[2][C], rest[2][C], beta[2][C];
-    LogSum G[2][C];
-    float gb[C];
+    float a[Cf::kAhead ? 2 : 1][C * kLdA];
+    float tmp[Cf::kAhead ? 2 : 1][32 * kLdT];
+    float gam[Cf::GSLOTS][C], rest[Cf::GSLOTS][C], beta[Cf::GSLOTS][C];
+    LogSum G[Cf::GSLOTS][C];
 };
 
 template <typename E, int DK, int W>
@@ -77,86 +76,132 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
         const E* k = static_cast<const E*>(a.k) + sq.rq * DK;
         const E* dO = static_cast<const E*>(a.dO) + sq.rv * a.dv + col0;
         Stage<E, DK, HT> sk, sq_;
-        Stage<E, Cf::COLS, HT> sd;
+        Stage<E, Cf::COLS, HT> s3;
         float g = 0.f, be = 0.f;
-        // chunk c of the sequence goes through buffer c & 1
-        auto load = [&](int c) {
-            const int t0 = c * C, rows = sq.len - t0;
-            sk.load(k + size_t(t0) * DK, DK, rows, ht);
-            sq_.load(q + size_t(t0) * DK, DK, rows, ht);
-            sd.load(dO + size_t(t0) * a.dv, a.dv, rows, ht);
-        };
+        // (chunks in the order of the recurrence: the c-th begins at this token)
+        auto token = [&](int c) { return (nc - 1 - c) * C; };
+        auto load_k = [&](int c) { sk.load(k + size_t(token(c)) * DK, DK, sq.len - token(c), ht); };
+        auto load_q = [&](int c) { sq_.load(q + size_t(token(c)) * DK, DK, sq.len - token(c), ht); };
+        auto load_3 = [&](int c) { s3.load(dO + size_t(token(c)) * a.dv, a.dv, sq.len - token(c), ht); };
         auto gates = [&](int c) {
-            const int t = c * C + (lane & 31);
+            const int t = token(c) + (lane & 31);
             g = t < sq.len ? load_gate(a.g, sq.rv + t, a.gate_bf16) : 0.f;
             be = t < sq.len ? load_gate(a.beta, sq.rv + t, a.gate_bf16) : 0.f;
         };
-        auto put = [&](int c) {
-            const int s = c & 1;
-            auto rows_into = [&](bf16_t* x) {
-                return [x](const Raw8<E>& r, int row, int p) {
-                    const auto y = planes_of<E>(r);
-#pragma unroll
-                    for (int n = 0; n < NP; ++n)
-                        *reinterpret_cast<bf16x8*>(x + n * C * DK + Cf::Tile::at(row, p)) = y.p[n];
-                };
-            };
-            sk.each(ht, rows_into(L.k[s]));
-            sq_.each(ht, rows_into(L.q[s]));
-            sd.each(ht, [&](const Raw8<E>& r, int row, int p) {
+        auto put_rows = [&](const Stage<E, DK, HT>& st, bf16_t* x) {
+            st.each(ht, [&](const Raw8<E>& r, int row, int p) {
                 const auto y = planes_of<E>(r);
 #pragma unroll
                 for (int n = 0; n < NP; ++n)
-                    *reinterpret_cast<bf16x8*>(L.d[s] + (n * C + row) * Cf::LDO + 8 * p) = y.p[n];
+                    *reinterpret_cast<bf16x8*>(x + n * C * DK + Cf::Tile::at(row, p)) = y.p[n];
             });
         };
-        auto prepare = [&](int c) {
-            const int s = c & 1;
+        auto put_k = [&](int c) { put_rows(sk, L.k[c % Cf::KSLOTS]); };
+        auto put_q = [&](int c) { put_rows(sq_, L.q[c % Cf::QSLOTS]); };
+        auto put_3 = [&](int c) {
+            s3.each(ht, [&](const Raw8<E>& r, int row, int p) {
+                const auto y = planes_of<E>(r);
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    *reinterpret_cast<bf16x8*>(L.d[c & 1] + (n * C + row) * Cf::LDO + 8 * p) = y.p[n];
+            });
+        };
+        auto sums = [&](int c) {
+            const int s = c % Cf::GSLOTS;
             const LogSum G = log_sums<C>(g, lane);
-            if (hw == 0) {
-                if (lane < C) {
-                    L.G[0][lane] = G;
-                    L.gb[lane] = be;
-                }
-                wave_lds_fence();
-                system_of<Cf, true>(L.k[s], L.G[0], L.gb, L.a, lane);
-                wave_lds_fence();
-                invert<true>(L.a, L.tmp, L.t[s], lane);
-            } else if (hw == 1) {
-                const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
-                if (lane < C) {
-                    L.G[1][lane] = G;
-                    L.gam[s][lane] = decay_of(G);
-                    L.rest[s][lane] = decay_between(last, G);
-                    L.beta[s][lane] = be;
-                }
-                wave_lds_fence();
-                readout_of<Cf, true, 3>(L.q[s], L.k[s], L.G[1], a.scale, C, L.p[s], lane);
+            const LogSum last = {lane_value(G.hi, 31), lane_value(G.lo, 31)};
+            if (lane < C) {
+                L.G[s][lane] = G;
+                L.gam[s][lane] = decay_of(G);
+                L.rest[s][lane] = decay_between(last, G);
+                L.beta[s][lane] = be;
             }
         };
-        int c = nc - 1;
-        if (nc > 0) {
-            load(c);
-            gates(c);
-            put(c);
-            if (nc > 1) load(c - 1);
-        }
-        sync_lds();
-        if (nc > 0) prepare(c);
-        if (nc > 1) {
-            gates(c - 1);
-            put(c - 1);
-        }
-        sync_lds();
-        for (; c >= 0; --c) {
-            if (c > 1) load(c - 2);
-            if (c > 0) {
-                prepare(c - 1);
-                if (c > 1) gates(c - 2);
+        auto system = [&](int c, int w) {
+            system_of<Cf, true>(L.k[c % Cf::KSLOTS], L.G[c % Cf::GSLOTS], L.beta[c % Cf::GSLOTS], L.a[w], lane);
+        };
+        auto inverse = [&](int c, int w) { invert<true>(L.a[w], L.tmp[w], L.t[c & 1], lane); };
+        auto readout = [&](int c) {
+            readout_of<Cf, true, 3>(L.q[c % Cf::QSLOTS], L.k[c % Cf::KSLOTS], L.G[c % Cf::GSLOTS], a.scale, C, L.p[c & 1], lane);
+        };
+        if constexpr (Cf::kAhead) {
+            // Interval c: rows of k go to LDS three chunks ahead, of q two, the third tensor's
+            // one; the waves take turns with a chunk's system and its inversion.
+            if (nc > 0) {
+                load_k(0);
+                gates(0);
+                put_k(0);
+                if (hw == 3) sums(0);
+                load_q(0);
+                load_3(0);
+            }
+            if (nc > 1) {
+                load_k(1);
+                gates(1);
             }
             sync_lds();
-            if (c > 1) put(c - 2);
+            for (int c = -2; c < nc; ++c) {
+                if (c + 3 < nc) {
+                    put_k(c + 3);
+                    if (hw == 3) sums(c + 3);
+                    if (c + 4 < nc) {
+                        load_k(c + 4);
+                        gates(c + 4);
+                    }
+                }
+                if (c + 2 < nc) {
+                    put_q(c + 2);
+                    if (c + 3 < nc) load_q(c + 3);
+                }
+                if (c >= -1 && c + 1 < nc) {
+                    put_3(c + 1);
+                    if (c + 2 < nc) load_3(c + 2);
+                }
+                if (hw == 2) {
+                    if (c >= -1 && c + 1 < nc) readout(c + 1);
+                } else if (hw < 2) {
+                    if ((c & 1) == hw) {
+                        if (c + 2 < nc) system(c + 2, hw);
+                    } else if (c >= -1 && c + 1 < nc) {
+                        inverse(c + 1, hw);
+                    }
+                }
+                sync_lds();
+            }
+        } else {
+            auto load = [&](int c) {
+                load_k(c);
+                load_q(c);
+                load_3(c);
+                gates(c);
+            };
+            auto put = [&](int c) {
+                put_k(c);
+                put_q(c);
+                put_3(c);
+                if (hw == 3) sums(c);
+            };
+            if (nc > 0) {
+                load(0);
+                put(0);
+                if (nc > 1) load(1);
+            }
             sync_lds();
+            for (int c = -1; c < nc; ++c) {
+                if (c >= 0 && c + 2 < nc) load(c + 2);
+                if (c + 1 < nc) {
+                    if (hw == 0) {
+                        system(c + 1, 0);
+                        wave_lds_fence();
+                        inverse(c + 1, 0);
+                    } else if (hw == 1) {
+                        readout(c + 1);
+                    }
+                }
+                sync_lds();  // chunk c is done with
+                if (c + 2 < nc) put(c + 2);
+                sync_lds();
+            }
         }
         return;
     }
@@ -175,8 +220,9 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
     float* part = a.part + size_t(col0 / 16 + wave) * a.rows + sq.rv;
     sync_lds();
     sync_lds();
+    sync_lds();
     for (int c = nc - 1; c >= 0; --c) {
-        const int s = c & 1, rows = sq.len - c * C;
+        const int at = nc - 1 - c, ks_ = at % Cf::KSLOTS, sg = at % Cf::GSLOTS, s = at & 1, rows = sq.len - c * C;
         const size_t row0 = size_t(c) * C + 8 * g;
         if (c == nc - 1 || (c + 1) % a.group == 0)
             keep_state<E, KS>(st, static_cast<E*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col0 + 16 * wave, lane);
@@ -188,7 +234,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
         for (int j = 0; j < KS; ++j) {
             const Planes<3> sp = state_planes<KT>(st, j);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) kd[x] = product<2>(row_frag<Cf>(L.k[s], x, j, lane), sp, kd[x]);
+            for (int x = 0; x < 2; ++x) kd[x] = product<2>(row_frag<Cf>(L.k[ks_], x, j, lane), sp, kd[x]);
         }
         Planes<NP> dp;  // dO, tokens along the contraction
 #pragma unroll
@@ -202,9 +248,9 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int t = 8 * g + 4 * x;
-            const floatx4 rs = *reinterpret_cast<const floatx4*>(&L.rest[s][t]);
-            const floatx4 bt = *reinterpret_cast<const floatx4*>(&L.beta[s][t]);
-            const floatx4 gm = *reinterpret_cast<const floatx4*>(&L.gam[s][t]);
+            const floatx4 rs = *reinterpret_cast<const floatx4*>(&L.rest[sg][t]);
+            const floatx4 bt = *reinterpret_cast<const floatx4*>(&L.beta[sg][t]);
+            const floatx4 gm = *reinterpret_cast<const floatx4*>(&L.gam[sg][t]);
             floatx4 u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -234,12 +280,12 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
             }
         }
         const Planes<3> yp = split8<3>(y), zp = split8<3>(z);
-        const float last = L.gam[s][C - 1];
+        const float last = L.gam[sg][C - 1];
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
             floatx4 w = {last * st[i][0], last * st[i][1], last * st[i][2], last * st[i][3]};
-            w = product<2>(col_frag<Cf>(L.k[s], i / 2, i % 2, lane), yp, w);
-            st[i] = product<2>(col_frag<Cf>(L.q[s], i / 2, i % 2, lane), zp, w);
+            w = product<2>(col_frag<Cf>(L.k[ks_], i / 2, i % 2, lane), yp, w);
+            st[i] = product<2>(col_frag<Cf>(L.q[at % Cf::QSLOTS], i / 2, i % 2, lane), zp, w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -247,7 +293,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
             if (m == i && 8 * g + i < rows) part[row0 + i] = db[i];
         }
         sync_lds();
-        sync_lds();
+        if constexpr (!Cf::kAhead) sync_lds();
     }
     if (a.dS0 != nullptr) store_state<KS>(st, a.dS0 + state, col, lane);
 }
