@@ -662,42 +662,52 @@ void forward_bf16(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
 }
 
 // ------------------------------------------------------------------- segments' states
-// starts[g + 1] <- M_g starts[g] + starts[g + 1] for g = 1 .. segs - 2 (starts[1] is there
-// already), in the order of the recurrence.  A workgroup takes 16 columns of a head's
-// states, a wave 32 rows of them; the state's planes meet in LDS, the next map is on its
-// way during a step.
-template <int DK>
-__global__ __launch_bounds__(2 * DK) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* starts) {
+// states[g + 1] += M_g states[g] for g = 1 .. segs - 2, or (BACK) states[g - 1] += M_g^T
+// states[g] for g = segs - 2 .. 1, in the order of the recurrence.  A workgroup takes 16
+// columns of a head's states, a wave 32 rows of them; the state's planes meet in LDS, the
+// next map is on its way during a step.
+template <int DK, bool BACK>
+__global__ __launch_bounds__(2 * DK) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* states) {
     constexpr int KS = DK / 32;
     __shared__ __align__(16) bf16x8 planes[2][KS][3][64];
     const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4;
     const size_t bh = blockIdx.x / unsigned(dv / 16), size = size_t(dv) * DK;
     const int col = int(blockIdx.x % unsigned(dv / 16)) * 16 + (lane & 15);
     const size_t mine = bh * size + size_t(col) * DK + 32 * wave + 8 * g;  // this lane's eight values of a state
+    const int steps = segs - 2;
+    auto seg = [&](int i) { return BACK ? segs - 2 - i : 1 + i; };  // whose map step i applies
+    auto next_of = [&](int i) { return BACK ? seg(i) - 1 : seg(i) + 1; };
     floatx4 st[2], next[2], m[2][KS][2];
     auto state = [&](int s, floatx4 (&x)[2]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x[h] = *reinterpret_cast<const floatx4*>(starts + size_t(s) * heads * size + mine + 4 * h);
+        for (int h = 0; h < 2; ++h) x[h] = *reinterpret_cast<const floatx4*>(states + size_t(s) * heads * size + mine + 4 * h);
     };
     auto map = [&](int s) {
-        const float* M = maps + ((s - 1) * size_t(heads) + bh) * size_t(DK) * DK + 8 * g;
+        const float* M = maps + ((s - 1) * size_t(heads) + bh) * size_t(DK) * DK;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
+            for (int j = 0; j < KS; ++j) {
+                const int row = 32 * wave + paired_row(lane, h), k = 32 * j + 8 * g;
 #pragma unroll
-                for (int v = 0; v < 2; ++v)
-                    m[h][j][v] = *reinterpret_cast<const floatx4*>(M + (32 * wave + paired_row(lane, h)) * DK + 32 * j + 4 * v);
+                for (int v = 0; v < 2; ++v) {
+                    if constexpr (!BACK) {
+                        m[h][j][v] = *reinterpret_cast<const floatx4*>(M + row * DK + k + 4 * v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[h][j][v][e] = M[(k + 4 * v + e) * DK + row];
+                    }
+                }
+            }
     };
-    state(1, st);
-    if (segs > 2) {
-        map(1);
-        state(2, next);
-    }
-    for (int s = 1; s < segs - 1; ++s) {
+    if (steps <= 0) return;
+    state(seg(0), st);
+    map(seg(0));
+    state(next_of(0), next);
+    for (int i = 0; i < steps; ++i) {
         const Planes<3> p = state_planes<2>(st, 0);
 #pragma unroll
-        for (int n = 0; n < 3; ++n) planes[s & 1][wave][n][lane] = p.p[n];
+        for (int n = 0; n < 3; ++n) planes[i & 1][wave][n][lane] = p.p[n];
         Planes<3> mp[2][KS];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -710,22 +720,29 @@ __global__ __launch_bounds__(2 * DK) void delta_compose_kernel(int heads, int dv
             }
         st[0] = next[0];
         st[1] = next[1];
-        if (s + 1 < segs - 1) {
-            map(s + 1);
-            state(s + 2, next);
+        if (i + 1 < steps) {
+            map(seg(i + 1));
+            state(next_of(i + 1), next);
         }
         sync_lds();
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
             Planes<3> q;
 #pragma unroll
-            for (int n = 0; n < 3; ++n) q.p[n] = planes[s & 1][j][n][lane];
+            for (int n = 0; n < 3; ++n) q.p[n] = planes[i & 1][j][n][lane];
 #pragma unroll
             for (int h = 0; h < 2; ++h) st[h] = product<2>(mp[h][j], q, st[h]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<floatx4*>(starts + size_t(s + 1) * heads * size + mine + 4 * h) = st[h];
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<floatx4*>(states + size_t(next_of(i)) * heads * size + mine + 4 * h) = st[h];
     }
+}
+
+template <int DK> void compose_dk(int heads, int dv, int segs, const float* maps, float* states, bool backward, hipStream_t st) {
+    const unsigned n = unsigned(heads) * unsigned(dv / 16);
+    if (backward) delta_compose_kernel<DK, true><<<n, 2 * DK, 0, st>>>(heads, dv, segs, maps, states);
+    else delta_compose_kernel<DK, false><<<n, 2 * DK, 0, st>>>(heads, dv, segs, maps, states);
 }
 
 // ------------------------------------------------------------------------- one token
@@ -873,6 +890,14 @@ Segments segments_of(const kdn_delta_desc* d, bool packed, int group) {
     return s;
 }
 
+hipError_t launch_compose(int heads, int dv, int dk, int segs, const float* maps, float* states, bool backward, hipStream_t st) {
+    if (segs <= 2) return hipSuccess;
+    if (dk == 32) compose_dk<32>(heads, dv, segs, maps, states, backward, st);
+    else if (dk == 64) compose_dk<64>(heads, dv, segs, maps, states, backward, st);
+    else compose_dk<128>(heads, dv, segs, maps, states, backward, st);
+    return hipGetLastError();
+}
+
 hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtype, int dk, hipStream_t st) {
     a.segs = s.count;
     if (s.count <= 1) return hipSuccess;
@@ -880,14 +905,9 @@ hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtyp
     a.maps = reinterpret_cast<float*>(static_cast<char*>(ws) + s.maps);
     if (dtype == KDN_BF16) forward_bf16(a, dk, MAPS, st);
     else forward_f32(a, dk, MAPS, st);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || s.count == 2) return e;
-    const int heads = a.B * a.H;
-    const unsigned n = unsigned(heads) * unsigned(a.dv / 16);
-    if (dk == 32) delta_compose_kernel<32><<<n, 64, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
-    else if (dk == 64) delta_compose_kernel<64><<<n, 128, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
-    else delta_compose_kernel<128><<<n, 256, 0, st>>>(heads, a.dv, a.segs, a.maps, a.starts);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_compose(a.B * a.H, a.dv, dk, a.segs, a.maps, a.starts, false, st);
 }
 
 hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st) {

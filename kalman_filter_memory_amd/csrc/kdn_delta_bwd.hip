@@ -35,9 +35,52 @@ struct BackwardArgs {
     size_t rows;        // tokens of all heads of values
     int B, H, Hk, T, dv;
     int group;
+    // segments (kdn_delta_launch.h): gradients of the states behind each, [segs] of them
+    int segs;
+    float* ends;
+    const float* maps;
     float scale;
     bool gate_bf16;
 };
+
+// A wave's columns through segment seg of a sequence.  MAPS: only the gradient of the state
+// in front of segments 1 .. segs - 1, from zero behind them (the last: from dS_T).
+struct Place {
+    int slice, h, b, seg;
+    size_t bh, heads;
+};
+template <bool MAPS> __device__ __forceinline__ Place place_of(const BackwardArgs& a, unsigned id, unsigned slices) {
+    Place p{};
+    p.heads = size_t(a.B) * a.H;
+    p.slice = int(id % slices);
+    id /= slices;
+    p.h = int(id % unsigned(a.H));
+    id /= unsigned(a.H);
+    p.b = int(id % unsigned(a.B));
+    p.seg = int(id / unsigned(a.B)) + (MAPS ? 1 : 0);
+    p.bh = size_t(p.b) * a.H + p.h;
+    return p;
+}
+template <bool MAPS, int KS>
+__device__ __forceinline__ void gradient_in(const BackwardArgs& a, const Place& p, floatx4 (&st)[2 * KS], int col, int lane) {
+    const size_t size = size_t(a.dv) * (32 * KS);
+    const bool last = p.seg == a.segs - 1;
+    // (the last segment ends in its own copy: dS0 may be dS_T's buffer)
+    const float* S = !MAPS && a.segs > 1 ? a.ends + p.seg * p.heads * size : MAPS && !last ? nullptr : a.dS_T;
+    if (S != nullptr) {
+        load_state<KS>(st, S + p.bh * size, col, lane);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (MAPS && last) store_state<KS>(st, a.ends + (p.seg * p.heads + p.bh) * size, col, lane);
+}
+template <bool MAPS, int KS>
+__device__ __forceinline__ void gradient_out(const BackwardArgs& a, const Place& p, const floatx4 (&st)[2 * KS], int col, int lane) {
+    const size_t size = size_t(a.dv) * (32 * KS);
+    if (MAPS) store_state<KS>(st, a.ends + ((p.seg - 1) * p.heads + p.bh) * size, col, lane);
+    else if (a.dS0 != nullptr && p.seg == 0) store_state<KS>(st, a.dS0 + p.bh * size, col, lane);
+}
 
 // ------------------------------------------------------------------ backward recurrence
 template <typename E, int DK, int W> struct ReverseLds {
@@ -51,20 +94,19 @@ template <typename E, int DK, int W> struct ReverseLds {
     LogSum G[Cf::GSLOTS][C];
 };
 
-template <typename E, int DK, int W>
+template <typename E, int DK, int W, bool MAPS>
 __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kernel(BackwardArgs a) {
     using Cf = Cfg<E, DK, W>;
     constexpr int NP = Cf::NP, KT = Cf::KT, KS = Cf::KS, HT = 64 * Cf::NH;
     __shared__ __align__(16) ReverseLds<E, DK, W> L;
 
-    const unsigned slices = unsigned(a.dv) / Cf::COLS;
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
-    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const Place at_ = place_of<MAPS>(a, xcd_order(blockIdx.x, gridDim.x), unsigned(a.dv) / Cf::COLS);
+    const int h = at_.h, b = at_.b;
+    Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int start = sq.start, c0 = cut_segment(sq, at_.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int col0 = slice * Cf::COLS;
-    const size_t state = (size_t(b) * a.H + h) * size_t(a.dv) * DK;
+    const int col0 = at_.slice * Cf::COLS;
 
     for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += Cf::kThreads)
         reinterpret_cast<u32x4*>(L.t)[i] = reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
@@ -208,13 +250,8 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
 
     const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
     floatx4 st[KT];
-    if (a.dS_T != nullptr) {
-        load_state<KS>(st, a.dS_T + state, col, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const size_t groups = group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C));
+    gradient_in<MAPS, KS>(a, at_, st, col, lane);
+    const size_t groups = group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group;
     const E* Ep = static_cast<const E*>(a.E) + sq.rv * a.dv + col;
     E* dV = static_cast<E*>(a.dv_out) + sq.rv * a.dv + col;
     float* part = a.part + size_t(col0 / 16 + wave) * a.rows + sq.rv;
@@ -224,11 +261,11 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
     for (int c = nc - 1; c >= 0; --c) {
         const int at = nc - 1 - c, ks_ = at % Cf::KSLOTS, sg = at % Cf::GSLOTS, s = at & 1, rows = sq.len - c * C;
         const size_t row0 = size_t(c) * C + 8 * g;
-        if (c == nc - 1 || (c + 1) % a.group == 0)
+        if (!MAPS && (c == nc - 1 || (c + 1) % a.group == 0))
             keep_state<E, KS>(st, static_cast<E*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(a.dv) * DK, col0 + 16 * wave, lane);
         float ev[8];  // E of this lane's tokens, 8 g + 0..7
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ev[e] = 8 * g + e < rows ? to_f<E>(Ep[(row0 + e) * a.dv]) : 0.f;
+        for (int e = 0; e < 8; ++e) ev[e] = !MAPS && 8 * g + e < rows ? to_f<E>(Ep[(row0 + e) * a.dv]) : 0.f;
         floatx4 kd[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
@@ -274,7 +311,7 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
                 const int i = 4 * x + e;
                 const float w = be[i] * xx[e];
                 db[i] = xx[e] * ev[i];
-                if (8 * g + i < rows) dV[(row0 + i) * a.dv] = from_f<E>(w);
+                if (!MAPS && 8 * g + i < rows) dV[(row0 + i) * a.dv] = from_f<E>(w);
                 y[i] = -gam[i] * w;
                 z[i] = a.scale * gam[i] * dof[i];
             }
@@ -287,15 +324,16 @@ __global__ __launch_bounds__((Cfg<E, DK, W>::kThreads)) void delta_reverse_kerne
             w = product<2>(col_frag<Cf>(L.k[ks_], i / 2, i % 2, lane), yp, w);
             st[i] = product<2>(col_frag<Cf>(L.q[at % Cf::QSLOTS], i / 2, i % 2, lane), zp, w);
         }
+        if constexpr (!MAPS)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            db[i] = group_sum<16>(db[i]);
-            if (m == i && 8 * g + i < rows) part[row0 + i] = db[i];
-        }
+            for (int i = 0; i < 8; ++i) {
+                db[i] = group_sum<16>(db[i]);
+                if (m == i && 8 * g + i < rows) part[row0 + i] = db[i];
+            }
         sync_lds();
         if constexpr (!Cf::kAhead) sync_lds();
     }
-    if (a.dS0 != nullptr) store_state<KS>(st, a.dS0 + state, col, lane);
+    gradient_out<MAPS, KS>(a, at_, st, col, lane);
 }
 
 // ---------------------------------------------------------------------- bfloat16 inputs
@@ -315,7 +353,7 @@ template <int DK, int DV> struct ReverseAheadLds {
     LogSum G[4][C];
 };
 
-template <int DK, int DV>
+template <int DK, int DV, bool MAPS>
 __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_reverse_ahead_kernel(BackwardArgs a) {
     using Lds = ReverseAheadLds<DK, DV>;
     constexpr int W = Lds::W, COLS = Lds::COLS;
@@ -323,14 +361,13 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
     constexpr int KT = Cf::KT, KS = Cf::KS;
     __shared__ __align__(16) Lds L;
 
-    constexpr unsigned slices = DV / COLS;
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int slice = int(id % slices), h = int(id / slices % unsigned(a.H)), b = int(id / slices / unsigned(a.H));
-    const Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const Place at_ = place_of<MAPS>(a, xcd_order(blockIdx.x, gridDim.x), DV / COLS);
+    const int h = at_.h, b = at_.b;
+    Seq sq = sequence(a.cu, b, h, a.H, a.Hk, a.T);
+    const int start = sq.start, c0 = cut_segment(sq, at_.seg, a.segs, a.group);
     const int nc = (sq.len + C - 1) / C;
     const int lane = threadIdx.x & 63, wave = wave_id();
-    const int col0 = slice * COLS;
-    const size_t state = (size_t(b) * a.H + h) * size_t(DV) * DK;
+    const int col0 = at_.slice * COLS;
 
     for (unsigned i = threadIdx.x; i < 2 * 3 * C * C / 8; i += 64 * (W + 4))
         reinterpret_cast<u32x4*>(L.t)[i] = reinterpret_cast<u32x4*>(L.p)[i] = u32x4{0, 0, 0, 0};
@@ -354,7 +391,7 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
                 copy_rows<DK, false>(k + size_t(c) * (C * DK), DK, rows, lk + s * (C * DK * 2), lane);
                 copy_rows<DK, false>(q + size_t(c) * (C * DK), DK, rows, lq + s * (C * DK * 2), lane);
                 copy_rows<COLS, true>(d + size_t(c) * (C * DV), DV, rows, ld + s * (C * COLS * 2), lane);
-                copy_rows<COLS, true>(e + size_t(c) * (C * DV), DV, rows, le + s * (C * COLS * 2), lane);
+                if constexpr (!MAPS) copy_rows<COLS, true>(e + size_t(c) * (C * DV), DV, rows, le + s * (C * COLS * 2), lane);
             };
             auto sums = [&](int i) {
                 const int s = i & 3;
@@ -412,13 +449,8 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
 
     const int g = lane >> 4, m = lane & 15, col = col0 + 16 * wave + m;
     floatx4 st[KT];
-    if (a.dS_T != nullptr) {
-        load_state<KS>(st, a.dS_T + state, col, lane);
-    } else {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) st[i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const size_t groups = group_slot(a.cu, b, sq.start, a.group * C, (a.T + a.group * C - 1) / (a.group * C));
+    gradient_in<MAPS, KS>(a, at_, st, col, lane);
+    const size_t groups = group_slot(a.cu, b, start, a.group * C, (a.T + a.group * C - 1) / (a.group * C)) + c0 / a.group;
     bf16_t* dV = static_cast<bf16_t*>(a.dv_out) + sq.rv * DV + col0 + 16 * wave + 4 * g;
     float* part = a.part + size_t(col0 / 16 + wave) * a.rows + sq.rv;
     bf16x8 plus[2], minus[2];
@@ -457,7 +489,7 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
     if (nc > 0) fetch(0);
     for (int i = 0; i < nc; ++i) {
         const int c = nc - 1 - i, s = i & 3;
-        if (i == 0 || (c + 1) % a.group == 0)
+        if (!MAPS && (i == 0 || (c + 1) % a.group == 0))
             keep_state<bf16_t, KS>(st, static_cast<bf16_t*>(a.D) + ((groups + c / a.group) * a.H + h) * size_t(DV) * DK,
                                    col0 + 16 * wave, lane);
         const float last = L.gam[s][C - 1];
@@ -495,7 +527,7 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) pd[x] = product<2>(pf[x], dp, pd[x]);
-        if (i > 0) results(c + 1, i == 1 ? sq.len - (nc - 1) * C : C);
+        if (!MAPS && i > 0) results(c + 1, i == 1 ? sq.len - (nc - 1) * C : C);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
             sp[j] = pack8(r1[2 * j], r1[2 * j + 1]);
@@ -562,8 +594,8 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
         if (i + 1 < nc) fetch((i + 1) & 3);
         sync_lds();
     }
-    if (nc > 0) results(0, nc == 1 ? sq.len : C);
-    if (a.dS0 != nullptr) store_state<KS>(st, a.dS0 + state, col, lane);
+    if (!MAPS && nc > 0) results(0, nc == 1 ? sq.len : C);
+    gradient_out<MAPS, KS>(a, at_, st, col, lane);
 }
 
 // -------------------------------------------------------------------------- gradients
@@ -938,11 +970,25 @@ __global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads), 2) void delta_grad_
 }
 
 // ---------------------------------------------------------------------------- launches
+void compose_backward(const BackwardArgs& a, int dk, hipStream_t st) {
+    launch_compose(int(a.B) * a.H, a.dv, dk, a.segs, a.maps, a.ends, true, st);
+}
 template <typename E, int DK, int DV> void backward_d(const BackwardArgs& a, size_t slots, hipStream_t st) {
     constexpr int W = DV == 32 ? 2 : 4;
     const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
-    if constexpr (sizeof(E) == 2) delta_reverse_ahead_kernel<DK, DV><<<n, 64 * (W + 4), 0, st>>>(a);
-    else delta_reverse_kernel<E, DK, W><<<n, Cfg<E, DK, W>::kThreads, 0, st>>>(a);
+    if constexpr (sizeof(E) == 2) {
+        if (a.segs > 1) {
+            delta_reverse_ahead_kernel<DK, DV, true><<<n * unsigned(a.segs - 1), 64 * (W + 4), 0, st>>>(a);
+            compose_backward(a, DK, st);
+        }
+        delta_reverse_ahead_kernel<DK, DV, false><<<n * unsigned(a.segs), 64 * (W + 4), 0, st>>>(a);
+    } else {
+        if (a.segs > 1) {
+            delta_reverse_kernel<E, DK, W, true><<<n * unsigned(a.segs - 1), Cfg<E, DK, W>::kThreads, 0, st>>>(a);
+            compose_backward(a, DK, st);
+        }
+        delta_reverse_kernel<E, DK, W, false><<<n * unsigned(a.segs), Cfg<E, DK, W>::kThreads, 0, st>>>(a);
+    }
     const unsigned groups = unsigned(slots * a.Hk);
     if (a.H > a.Hk) delta_grad_kernel<E, DK, DV, true><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
     else delta_grad_kernel<E, DK, DV, false><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
@@ -959,7 +1005,7 @@ template <typename E> void backward_e(const BackwardArgs& a, int dk, size_t slot
 }
 
 struct Layout {
-    size_t E, S, D, part, segments, total;
+    size_t E, S, D, part, segments, ends, total;
     size_t rows, slots;
     Segments seg;
 };
@@ -975,7 +1021,8 @@ Layout layout_of(const kdn_delta_desc* d, bool packed) {
     l.part = l.D + up(l.slots * d->H * d->d_v * d->d_k * e);
     l.segments = l.part + up(l.rows * (d->d_v / 16) * 4);
     l.seg = segments_of(d, packed, kept_chunks(d->dtype));
-    l.total = l.segments + l.seg.total;
+    l.ends = l.segments + up(l.seg.total);
+    l.total = l.seg.count > 1 ? l.ends + size_t(l.seg.count) * d->B * d->H * d->d_v * d->d_k * 4 : l.segments + 16;
     return l;
 }
 
@@ -1067,6 +1114,9 @@ kdn_status kdn_gated_delta_backward(const kdn_delta_desc* d, const int32_t* cu_s
     a.group = f.group;
     a.scale = d->scale;
     a.gate_bf16 = f.gate_bf16;
+    a.segs = l.seg.count;
+    a.ends = reinterpret_cast<float*>(w + l.ends);
+    a.maps = f.maps;
     if (d->dtype == KDN_BF16) backward_e<kdn::bf16_t>(a, d->d_k, l.slots, st);
     else backward_e<float>(a, d->d_k, l.slots, st);
     return hipGetLastError() == hipSuccess ? KDN_OK : KDN_ERR_HIP;

@@ -53,6 +53,10 @@ Segments segments_of(const kdn_delta_desc* d, bool packed, int group);
 // The states in front of all segments, in a.starts, from a.S0; sets a.segs and the pointers
 hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtype, int dk, hipStream_t st);
 
+// states[g + 1] += M_g states[g] for g = 1 .. segs - 2, or, backward, states[g - 1] +=
+// M_g^T states[g] for g = segs - 2 .. 1 (a state of all heads each)
+hipError_t launch_compose(int heads, int dv, int dk, int segs, const float* maps, float* states, bool backward, hipStream_t st);
+
 kdn_status check(const kdn_delta_desc* d, bool one_token);
 hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hipStream_t st);
 hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st);

@@ -59,12 +59,43 @@ def test_matches_the_formula(shape, kind):
         assert torch.equal(got[n], again[n]), n
 
 
-@pytest.mark.parametrize("shape", [(1, 1, 1, 1500, 64, 64, "f32", "f32"), (1, 2, 1, 1203, 128, 32, "bf16", "f32")])
+@pytest.mark.parametrize("shape", [
+    (1, 1, 1, 1500, 64, 64, "f32", "f32"), (1, 2, 1, 1203, 128, 32, "bf16", "f32"), (1, 1, 1, 1100, 128, 128, "bf16", "bf16"),
+    (1, 2, 2, 1300, 32, 64, "bf16", "f32"), (1, 1, 1, 1001, 128, 64, "f32", "f32")])
 def test_few_heads_over_long_sequences(shape):
+    """Both recurrences cut into segments, also with dS0 over dS_T's own buffer"""
     x, do, S0, dS_T = _all(shape, 52)
+    B, H, Hk, T, dk, dv, dtype, gate = shape
+    code = {"f32": kdn.F32, "bf16": kdn.BF16}
+    few, many = (kdn.make_delta_desc(b, H, Hk, T, dk, dv, code[dtype], code[gate]) for b in (1, 512))
+    need = [kdn.load_library().kdn_gated_delta_backward_workspace_bytes(ctypes.byref(d), 0) for d in (few, many)]
+    assert need[0] > 1.02 * need[1] / 512  # (maps and states of segments)
     say(f"[gpu] gated_delta_backward in segments {shape}")
     got = kdn.gated_delta_backward(*x, do, S0, dS_T)
     _check(got, *rounding_bounds(*x, do, S0, dS_T, HALF[x[2].dtype]), x[2].dtype)
+    out = {n: torch.empty_like(t) for n, t in got.items()}
+    out["dS0"] = dS_T.clone()
+    kdn.gated_delta_backward(*x, do, S0, out["dS0"], out=out)
+    for n in NAMES:
+        assert torch.equal(out[n], got[n]), n
+
+
+def test_long_packed_sequences_of_few_heads():
+    lengths = (700, 3, 0, 900, 33)
+    x, do, _, _ = _all((1, 1, 1, sum(lengths), 64, 64, "f32", "f32"), 18)
+    x, do = [t[0] for t in x], do[0]
+    cu = torch.tensor([0, *torch.tensor(lengths).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+    S0, dS_T = torch.randn(2, len(lengths), 1, 64, 64, device="cuda")
+    got = kdn.gated_delta_backward(*x, do, S0, dS_T, cu_seqlens=cu)
+    at = 0
+    for i, n in enumerate(lengths):
+        part = [t[None, :, at:at + n].contiguous() for t in (*x, do)]
+        one = {m: got[m][None, :, at:at + n] for m in NAMES[:5]} | {"dS0": got["dS0"][i:i + 1]}
+        if n:
+            _check(one, delta_gradients(*part, S0[i:i + 1], dS_T[i:i + 1]), {}, torch.float32)
+        else:
+            assert torch.equal(got["dS0"][i], dS_T[i])
+        at += n
 
 
 def test_without_states_and_with_another_scale():
