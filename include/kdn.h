@@ -630,8 +630,9 @@ kdn_status kdn_gated_delta(const kdn_delta_desc *d, const int32_t *cu_seqlens, c
  * bfloat16 the operands of the last products (corrections, states at every 64th
  * token, dv and their weights) are rounded to bfloat16, which costs dq, dk, dg and
  * dbeta a few of their own roundings; dv and dS0 carry none of it.  dS0 may be
- * dS_T's buffer; no other output may alias an input.  Fewer than 2^23 groups of 64
- * tokens (float32: 32) of all heads of keys (KDN_ERR_UNSUPPORTED otherwise).
+ * dS_T's buffer; no other output may alias an input.  Heads of keys without any of
+ * values: KDN_ERR_SHAPE.  Fewer than 2^23 groups of 64 tokens (float32: 32) of all
+ * heads of keys (KDN_ERR_UNSUPPORTED otherwise).
  * packed: whether cu_seqlens will be given.  Every pointer but g, beta, dg, dbeta
  * and cu_seqlens 16-byte aligned. */
 size_t kdn_gated_delta_backward_workspace_bytes(const kdn_delta_desc *d, int32_t packed);

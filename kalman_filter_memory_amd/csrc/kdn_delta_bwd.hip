@@ -1030,6 +1030,7 @@ Layout layout_of(const kdn_delta_desc* d, bool packed) {
 kdn_status check_backward(const kdn_delta_desc* d, bool packed) {
     const kdn_status c = check(d, false);
     if (c != KDN_OK) return c;
+    if (d->H == 0 && d->Hk > 0) return KDN_ERR_SHAPE;  // (no head of values writes their gradients)
     return layout_of(d, packed).slots * size_t(d->Hk) >= (size_t(1) << 23) ? KDN_ERR_UNSUPPORTED : KDN_OK;
 }
 
