@@ -833,8 +833,8 @@ template <typename E, typename G> void step_dk(const StepArgs& a, int dk, int dv
 
 // no tokens: the states pass through
 __global__ __launch_bounds__(256) void delta_states_kernel(size_t n, const float* in, float* out) {
-    const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) out[i] = in != nullptr ? in[i] : 0.f;
+    for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += size_t(gridDim.x) * 256)
+        out[i] = in != nullptr ? in[i] : 0.f;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -912,7 +912,7 @@ hipError_t launch_segments(ForwardArgs& a, const Segments& s, void* ws, int dtyp
 
 hipError_t launch_states(size_t n, const float* in, float* out, hipStream_t st) {
     if (n == 0 || out == nullptr || in == out) return hipSuccess;
-    delta_states_kernel<<<unsigned((n + 255) / 256), 256, 0, st>>>(n, in, out);
+    delta_states_kernel<<<unsigned(std::min<size_t>((n + 255) / 256, 1 << 16)), 256, 0, st>>>(n, in, out);
     return hipGetLastError();
 }
 
