@@ -1211,6 +1211,9 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, q_weight, k_weight, position, 
         dq, dk = out
         _shaped("dq", dq, q.dtype, q.shape)
         _shaped("dk", dk, q.dtype, k.shape)
+        for name, x in (("dq", dq), ("dk", dk)):
+            if any(s == 0 and n > 1 for s, n in zip(x.stride(), x.shape)):
+                raise ValueError(f"{name} must not overlap itself")
     at = dev.index
     n = _rotary_desc(q, k, q_weight, k_weight, position, inv_freq, 0.0, interleaved, at,
                      (*_row_strides("dq", dq, at), *_row_strides("dk", dk, at)))

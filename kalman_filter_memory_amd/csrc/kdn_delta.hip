@@ -16,7 +16,10 @@ namespace {
 // The columns of S are independent, so a wave carries 16 of them through the sequence
 // alone, in registers; the results of one product are the operands of the next without
 // any exchange (paired_row).  Four more waves load the chunks into LDS and prepare T and
-// P a chunk ahead, which do not depend on the state.
+// P ahead, which do not depend on the state.  This one is for float32 (three planes of every
+// row); delta_ahead_kernel is for bfloat16.  Bound by the chain of dependent products of a
+// chunk, not by HBM: 19.6 us for 5 chunks of 4 heads at d 64, the pipeline's fill among them,
+// where the 0.75 MB would take 0.15.
 // KEEP: instead of o, the corrections E and the states that the backward pass needs.  MAPS:
 // nothing but the state behind a segment, from the zero state (segment 0: the first one),
 // and beside it, by as many waves again, from the unit matrix with v = 0.
@@ -385,6 +388,13 @@ void forward_f32(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
 //   helper 2       forms P of chunk c + 1
 //   helpers 0, 1   form the triangular system of chunk c + 2, and invert that of c + 1,
 //                  taking turns (a chunk stays with one of them)
+// Measured, d 128, B 8, H 16, T 4096: 239 to 290 us (with T and P one chunk ahead behind two
+// barriers, and rows through registers, 416), where the 558 MB take 109 at a copy's rate and
+// the products 41 at the matrix unit's.  The bound is a chunk's chain, 1.9 us: about 82
+// dependent matrix and 200 vector instructions of one wave per SIMD, which shares its SIMD with
+// a helper (matrix unit busy 39 % of the time, vector issue 50 %).  Slices of 64 columns: those
+// of 128 spill (988 against 515 us at B 16, H 16); of 32 would prepare every chunk four times.
+// Four places in LDS: five gained nothing.
 template <int DK, int DV, int MODE> struct AheadLds {
     static constexpr int W = DV == 32 || DK == 32 ? 2 : 4, COLS = 16 * W;
     bf16_t k[4][C * DK];
@@ -665,7 +675,8 @@ void forward_bf16(const ForwardArgs& a, int dk, int mode, hipStream_t st) {
 // states[g + 1] += M_g states[g] for g = 1 .. segs - 2, or (BACK) states[g - 1] += M_g^T
 // states[g] for g = segs - 2 .. 1, in the order of the recurrence.  A workgroup takes 16
 // columns of a head's states, a wave 32 rows of them; the state's planes meet in LDS, the
-// next map is on its way during a step.
+// next map is on its way during a step.  Bound by latency: 20 us for 6 steps of 16 heads at
+// d 128 (one wave per 16 columns, its maps loaded when needed: 114).
 template <int DK, bool BACK>
 __global__ __launch_bounds__(2 * DK) void delta_compose_kernel(int heads, int dv, int segs, const float* __restrict__ maps, float* states) {
     constexpr int KS = DK / 32;
@@ -747,7 +758,9 @@ template <int DK> void compose_dk(int heads, int dv, int segs, const float* maps
 
 // ------------------------------------------------------------------------- one token
 // d_k / 4 lanes per row of S, four elements each; a workgroup owns one state, every wave
-// d_v / NW of its rows.  Bound by the state's 8 d_k d_v bytes.
+// d_v / NW of its rows, all of which are on their way before the first is used.  Bound by the
+// state's 8 d_k d_v bytes: 256 x 16 states of 128 x 128 in 80 us, 6.7 TB/s (above a copy's
+// rate: 268 MB of states stay partly in the last-level cache); one sequence's 16 in 3.7.
 template <int DK, int DV> struct StepCfg {
     static constexpr int LPR = DK / 4, RPS = 64 / LPR;
     static constexpr int NW = DV / RPS < 8 ? DV / RPS : 8, RPW = DV / NW, SLOTS = RPW / RPS;
@@ -861,7 +874,9 @@ hipError_t launch_forward(const ForwardArgs& a, int dtype, int dk, bool keep, hi
 
 // The count is chosen by an estimate of the launches' rounds of 256 workgroups: a chunk of
 // 32 tokens takes 1.9 us with the read-out and 2.3 in the maps (d 128, bfloat16), a step of
-// the composition 1.5 us, two more launches 8.
+// the composition 1.5 us, two more launches 8; segments have to win a fifth.  Measured, d 128,
+// bfloat16, 1 x 16 x 65536: 0.99 ms in 8 segments, 3.35 in one piece.  Unit columns of the
+// maps in workgroups of their own would prepare each chunk twice: 893 against 738 us for them.
 Segments segments_of(const kdn_delta_desc* d, bool packed, int group) {
     Segments s{};
     s.count = 1;

@@ -101,6 +101,19 @@ def test_rotary_beyond_32_bit_offsets():
     assert torch.equal(dq[:, -n:], eq) and torch.equal(dk[:, -n:], ek) and torch.isfinite(dw).all()
 
 
+def test_rotary_refuses_outputs_that_overlap():
+    q, k = torch.randn(1, 4, 2, 32, device="cuda"), torch.randn(1, 4, 1, 32, device="cuda")
+    w = torch.ones(32, device="cuda")
+    qo, ko, qr, kr = kdn.qk_norm_rotary(q, k, w, w, None, None)
+    one = torch.empty(1, 4, 1, 32, device="cuda")
+    with pytest.raises(ValueError):
+        kdn.qk_norm_rotary_backward(qo, ko, q, k, w, w, None, None, qr, kr, out=(one.expand(1, 4, 2, 32), torch.empty_like(k)))
+    # heads that share their rows are fine to read
+    shared = one.normal_().expand(1, 4, 2, 32)
+    a, b = kdn.qk_norm_rotary(shared, k, w, w, None, None), kdn.qk_norm_rotary(shared.contiguous(), k, w, w, None, None)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def _run(x, S0, dO):
     o, S_T = kdn.gated_delta(*x, S0)
     return [o, S_T, *kdn.gated_delta_backward(*x, dO, S0, S0).values()]
