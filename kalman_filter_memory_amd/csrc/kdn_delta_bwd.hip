@@ -612,11 +612,15 @@ __global__ __launch_bounds__(64 * (ReverseAheadLds<DK, DV>::W + 4)) void delta_r
 // columns.  d_v is taken PASS columns at a time.  Bound by HBM and, less, by its vector
 // instructions: 400 to 435 us at d 128, bfloat16, B 8, H 16, T 4096 for 1.52 GB, 3.6 TB/s.
 // (Tokens down, U formed in LDS, 16 columns to each of eight waves: 996.)
-template <typename E, int DK, int DV> struct GradCfg {
+template <typename E, int DK, int DV, bool SHARED> struct GradCfg {
     static constexpr bool kPlain = sizeof(E) == 2;
     static constexpr int NP = kPlain ? 1 : 3;
     static constexpr int G = kPlain ? 64 : 32;  // tokens of a group
-    static constexpr int TD = DK == 128 ? 2 : 1;
+    // (bfloat16 with shared heads: the sums over them would spill beside two tiles of key
+    // dimensions a wave; float32 has half the tokens, and reads its planes half as often.  8 x 16
+    // heads on 4, 4096 tokens, d 128, the whole backward: 951 us, with two 1029; float32,
+    // 4 x 16 on 4, 2048 tokens: 953 with two, 1033)
+    static constexpr int TD = DK == 128 && !(SHARED && kPlain) ? 2 : 1;
     static constexpr int NW = DK / 16 / TD, kThreads = 64 * NW;
     static constexpr int PASS = kPlain && DV > 32 ? 64 : 32, kPasses = DV / PASS, NS = PASS / 32;
     static constexpr int NJ = G / 32, NX = 2 * NJ;           // pairs of token tiles, tiles
@@ -626,8 +630,8 @@ template <typename E, int DK, int DV> struct GradCfg {
     using VRow = Rows<PASS>;
     using MRow = Rows<G>;
 };
-template <typename E, int DK, int DV> struct GradLds {
-    using Cf = GradCfg<E, DK, DV>;
+template <typename E, int DK, int DV, bool SHARED> struct GradLds {
+    using Cf = GradCfg<E, DK, DV, SHARED>;
     static constexpr int kTile = Cf::NP * Cf::G * Cf::PASS, kSquare = Cf::NP * Cf::G * Cf::G;
     bf16_t q[Cf::NP * Cf::G * DK], k[Cf::NP * Cf::G * DK];
     union {
@@ -686,9 +690,9 @@ __device__ __forceinline__ void rows_to_lds(const E* x, unsigned stride, int row
 
 // SHARED: several heads of values share the head of keys.
 template <typename E, int DK, int DV, bool SHARED>
-__global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads), 2) void delta_grad_kernel(BackwardArgs a) {
-    using Cf = GradCfg<E, DK, DV>;
-    using Lds = GradLds<E, DK, DV>;
+__global__ __launch_bounds__((GradCfg<E, DK, DV, SHARED>::kThreads), 2) void delta_grad_kernel(BackwardArgs a) {
+    using Cf = GradCfg<E, DK, DV, SHARED>;
+    using Lds = GradLds<E, DK, DV, SHARED>;
     constexpr int NP = Cf::NP, G = Cf::G, NW = Cf::NW, NJ = Cf::NJ, NX = Cf::NX, NS = Cf::NS, LIM = NP - 1, TD = Cf::TD;
     constexpr int PASS = Cf::PASS, NB = Cf::NB, NBLK = Cf::NBLK, KSIZE = G * DK, VSIZE = G * PASS, MSIZE = G * G;
     __shared__ __align__(16) Lds L;
@@ -978,38 +982,42 @@ __global__ __launch_bounds__((GradCfg<E, DK, DV>::kThreads), 2) void delta_grad_
 }
 
 // ---------------------------------------------------------------------------- launches
-void compose_backward(const BackwardArgs& a, int dk, hipStream_t st) {
-    launch_compose(int(a.B) * a.H, a.dv, dk, a.segs, a.maps, a.ends, true, st);
+hipError_t compose_backward(const BackwardArgs& a, int dk, hipStream_t st) {
+    const hipError_t e = hipGetLastError();  // of the maps' launch
+    return e != hipSuccess ? e : launch_compose(int(a.B) * a.H, a.dv, dk, a.segs, a.maps, a.ends, true, st);
 }
-template <typename E, int DK, int DV> void backward_d(const BackwardArgs& a, size_t slots, hipStream_t st) {
+template <typename E, int DK, int DV> hipError_t backward_d(const BackwardArgs& a, size_t slots, hipStream_t st) {
     constexpr int W = DV == 32 ? 2 : 4;
     const unsigned n = unsigned(a.B) * unsigned(a.H) * unsigned(DV / (16 * W));
     if constexpr (sizeof(E) == 2) {
         if (a.segs > 1) {
             delta_reverse_ahead_kernel<DK, DV, true><<<n * unsigned(a.segs - 1), 64 * (W + 4), 0, st>>>(a);
-            compose_backward(a, DK, st);
+            const hipError_t e = compose_backward(a, DK, st);
+            if (e != hipSuccess) return e;
         }
         delta_reverse_ahead_kernel<DK, DV, false><<<n * unsigned(a.segs), 64 * (W + 4), 0, st>>>(a);
     } else {
         if (a.segs > 1) {
             delta_reverse_kernel<E, DK, W, true><<<n * unsigned(a.segs - 1), Cfg<E, DK, W>::kThreads, 0, st>>>(a);
-            compose_backward(a, DK, st);
+            const hipError_t e = compose_backward(a, DK, st);
+            if (e != hipSuccess) return e;
         }
         delta_reverse_kernel<E, DK, W, false><<<n * unsigned(a.segs), Cfg<E, DK, W>::kThreads, 0, st>>>(a);
     }
     const unsigned groups = unsigned(slots * a.Hk);
-    if (a.H > a.Hk) delta_grad_kernel<E, DK, DV, true><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
-    else delta_grad_kernel<E, DK, DV, false><<<groups, GradCfg<E, DK, DV>::kThreads, 0, st>>>(a);
+    if (a.H > a.Hk) delta_grad_kernel<E, DK, DV, true><<<groups, GradCfg<E, DK, DV, true>::kThreads, 0, st>>>(a);
+    else delta_grad_kernel<E, DK, DV, false><<<groups, GradCfg<E, DK, DV, false>::kThreads, 0, st>>>(a);
+    return hipGetLastError();
 }
-template <typename E, int DK> void backward_k(const BackwardArgs& a, size_t slots, hipStream_t st) {
-    if (a.dv == 32) backward_d<E, DK, 32>(a, slots, st);
-    else if (a.dv == 64) backward_d<E, DK, 64>(a, slots, st);
-    else backward_d<E, DK, 128>(a, slots, st);
+template <typename E, int DK> hipError_t backward_k(const BackwardArgs& a, size_t slots, hipStream_t st) {
+    if (a.dv == 32) return backward_d<E, DK, 32>(a, slots, st);
+    if (a.dv == 64) return backward_d<E, DK, 64>(a, slots, st);
+    return backward_d<E, DK, 128>(a, slots, st);
 }
-template <typename E> void backward_e(const BackwardArgs& a, int dk, size_t slots, hipStream_t st) {
-    if (dk == 32) backward_k<E, 32>(a, slots, st);
-    else if (dk == 64) backward_k<E, 64>(a, slots, st);
-    else backward_k<E, 128>(a, slots, st);
+template <typename E> hipError_t backward_e(const BackwardArgs& a, int dk, size_t slots, hipStream_t st) {
+    if (dk == 32) return backward_k<E, 32>(a, slots, st);
+    if (dk == 64) return backward_k<E, 64>(a, slots, st);
+    return backward_k<E, 128>(a, slots, st);
 }
 
 struct Layout {
@@ -1034,7 +1042,7 @@ Layout layout_of(const kdn_delta_desc* d, bool packed) {
     return l;
 }
 
-// the gradient kernel's workgroups stay within a launch
+// the gradient kernel's workgroups, of 512 threads at most, stay within a launch
 kdn_status check_backward(const kdn_delta_desc* d, bool packed) {
     const kdn_status c = check(d, false);
     if (c != KDN_OK) return c;
@@ -1126,9 +1134,8 @@ kdn_status kdn_gated_delta_backward(const kdn_delta_desc* d, const int32_t* cu_s
     a.segs = l.seg.count;
     a.ends = reinterpret_cast<float*>(w + l.ends);
     a.maps = f.maps;
-    if (d->dtype == KDN_BF16) backward_e<kdn::bf16_t>(a, d->d_k, l.slots, st);
-    else backward_e<float>(a, d->d_k, l.slots, st);
-    return hipGetLastError() == hipSuccess ? KDN_OK : KDN_ERR_HIP;
+    const hipError_t e = d->dtype == KDN_BF16 ? backward_e<kdn::bf16_t>(a, d->d_k, l.slots, st) : backward_e<float>(a, d->d_k, l.slots, st);
+    return e == hipSuccess ? KDN_OK : KDN_ERR_HIP;
 }
 
 }  // extern "C"
